@@ -29,7 +29,8 @@ WQ_F32, WQ_F16, WQ_BF16, WQ_I8, WQ_I32 = range(5)
 EXPORTED = ("wq_quantize_pack", "wq_quantize_workspace_size", "wq_unpack", "act_quant_int8", "w4a16_gemm",
             "w4a16_gemm_noalloc", "w4a8_gemm", "wq_workspace_size", "wq_status_string", "wq_last_error",
             "wq_graph_create", "wq_graph_set_io", "wq_graph_launch", "wq_graph_destroy", "w4a8_gemm_fused",
-            "wq_repack", "act_quant_fp8", "w8a8_fp8_gemm", "w8a8_fp8_gemm_fused")
+            "wq_repack", "act_quant_fp8", "w8a8_fp8_gemm", "w8a8_fp8_gemm_fused", "rmsnorm_quant_int8",
+            "rmsnorm_quant_fp8", "kv_append", "kv_attention", "kv_attention_workspace_size")
 
 
 class WqError(RuntimeError):
@@ -45,6 +46,7 @@ class QConfig(ctypes.Structure):
 
 LAYOUT_NT, LAYOUT_NATIVE = 0, 1
 FMT_INT, FMT_E2M1, FMT_E4M3 = 0, 1, 2
+ROPE_HALF, ROPE_PAIRS = 0, 1
 
 
 @dataclass(frozen=True)
@@ -75,6 +77,17 @@ class MatmulDesc(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("C", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("c", QConfig)]
+
+
+class _KVCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class _KVBatchC(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
 
 
 _lib = None
@@ -122,6 +135,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.wq_last_error.restype = ctypes.c_char_p
     lib.wq_device_error.argtypes = []
     lib.wq_device_error.restype = ctypes.c_int
+    pc, pb = ctypes.POINTER(_KVCacheC), ctypes.POINTER(_KVBatchC)
+    f32, i32 = ctypes.c_float, ctypes.c_int32
+    for f in (lib.rmsnorm_quant_int8, lib.rmsnorm_quant_fp8):
+        f.argtypes, f.restype = [vp, vp, vp, st, f32, i64, i64, vp, vp, vp, vp], st
+    lib.kv_append.argtypes = [vp, st, i64, i32, vp, i64, i32, i32, vp, pc, pb, vp]
+    lib.kv_append.restype = st
+    lib.kv_attention.argtypes = [vp, st, i64, i32, pc, pb, f32, vp, vp, sz, vp]
+    lib.kv_attention.restype = st
+    lib.kv_attention_workspace_size.argtypes = [i64, i32, pc, pb]
+    lib.kv_attention_workspace_size.restype = sz
     lib.wq_graph_create.argtypes = [ctypes.POINTER(MatmulDesc), ctypes.c_int, ctypes.POINTER(ctypes.c_void_p)]
     lib.wq_graph_create.restype = st
     lib.wq_graph_set_io.argtypes = [vp, ctypes.c_int, vp, vp]
@@ -392,6 +415,197 @@ def w4a8_gemm_fused(A, Wq, scales, zeros, N: int, K: int, qc: QuantConfig, bias=
                                         wsb, _stream(stream))
     _check(rc, "w4a8_gemm_fused")
     return C, Aq, sc
+
+
+# ---------------------------------------------------------------- a layer's steps between its matmuls
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other arguments are on {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _want(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+class _Call:
+    """The tensors' device made current, and a stream of that device (the given one or its current
+    one).  Outputs are made on that stream, so that the allocator orders their reuse by it."""
+
+    def __init__(self, device, stream):
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        if self.stream.device != device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors are on {device}")
+        self._guard = None
+        if torch.cuda.current_device() != device.index or stream is not None:
+            self._guard = torch.cuda.stream(self.stream)  # also makes the stream's device current
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _rmsnorm_quant(name, code_dtype, X, gamma, eps, residual, out_residual, out_q, out_scale, stream):
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("X must be float16 or bfloat16")
+    _same_device(X.device, X=X, gamma=gamma, residual=residual, out_residual=out_residual, out_q=out_q,
+                 out_scale=out_scale)
+    M, K = X.shape
+    _want(gamma, "gamma", X.dtype, (K,))
+    if residual is not None:
+        _want(residual, "residual", X.dtype, (M, K))
+    elif out_residual is not None:
+        raise ValueError("out_residual needs residual")
+    with _Call(X.device, stream) as s:
+        h = None
+        if residual is not None:
+            h = out_residual if out_residual is not None else torch.empty_like(X)
+            _want(h, "out_residual", X.dtype, (M, K))
+        q = out_q if out_q is not None else torch.empty(M, K, dtype=code_dtype, device=X.device)
+        sc = out_scale if out_scale is not None else torch.empty(M, dtype=torch.float32, device=X.device)
+        _want(q, "out_q", code_dtype, (M, K))
+        _want(sc, "out_scale", torch.float32, (M,))
+        rc = getattr(load_library(), name)(_ptr(X), _ptr(residual), _ptr(gamma), _DT[X.dtype], eps, M, K, _ptr(h),
+                                           _ptr(q), _ptr(sc), s)
+    _check(rc, name)
+    return q, sc, h
+
+
+def rmsnorm_quant_int8(X, gamma, eps: float, residual=None, out_residual=None, out_q=None, out_scale=None,
+                       stream=None):
+    """RMS norm of X [M,K] fp16/bf16 (plus ``residual``), quantized per token to INT8.
+
+    Returns (Aq int8 [M,K], a_scale fp32 [M], h): h is X + residual in X's dtype (None without a
+    residual; ``out_residual`` may be X or residual itself).  Aq and a_scale are what
+    :func:`w4a8_gemm` takes."""
+    return _rmsnorm_quant("rmsnorm_quant_int8", torch.int8, X, gamma, eps, residual, out_residual, out_q, out_scale,
+                          stream)
+
+
+def rmsnorm_quant_fp8(X, gamma, eps: float, residual=None, out_residual=None, out_q=None, out_scale=None, stream=None):
+    """As :func:`rmsnorm_quant_int8` with e4m3 codes (uint8 [M,K]), for :func:`w8a8_fp8_gemm`."""
+    return _rmsnorm_quant("rmsnorm_quant_fp8", torch.uint8, X, gamma, eps, residual, out_residual, out_q, out_scale,
+                          stream)
+
+
+class KVCache:
+    """A paged key / value cache in 8 bits (wq_kv_cache): ``k``, ``v`` [num_pages, kv_heads,
+    page_size, pitch] int8, or e4m3 codes as uint8 / float8_e4m3fn, with pitch = head_dim rounded up
+    to a multiple of 16, and ``k_scale``, ``v_scale`` fp32 [num_pages, kv_heads]."""
+
+    def __init__(self, k, v, k_scale, v_scale, head_dim: int):
+        _same_device(k.device, k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+        if k.dim() != 4 or k.shape[3] != -(-head_dim // 16) * 16:
+            raise ValueError("k must be [num_pages, kv_heads, page_size, head_dim rounded up to a multiple of 16]")
+        if k.dtype not in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+            raise ValueError("k must be int8 (INT8 codes), uint8 or float8_e4m3fn (e4m3 codes)")
+        _want(v, "v", k.dtype, k.shape)
+        _want(k_scale, "k_scale", torch.float32, k.shape[:2])
+        _want(v_scale, "v_scale", torch.float32, k.shape[:2])
+        self.k, self.v, self.k_scale, self.v_scale, self.head_dim = k, v, k_scale, v_scale, head_dim
+        self.device, self.kv_heads = k.device, k.shape[1]
+        self.format = FMT_INT if k.dtype == torch.int8 else FMT_E4M3
+        self._c = _KVCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[0], k.shape[2],
+                            k.shape[1], head_dim, self.format)
+
+
+def make_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, format: int = FMT_INT,
+                  device=None) -> KVCache:
+    """A new cache of INT8 (FMT_INT) or e4m3 (FMT_E4M3) codes."""
+    device = device or "cuda"
+    shape = (num_pages, kv_heads, page_size, -(-head_dim // 16) * 16)
+    dt = torch.int8 if format == FMT_INT else torch.uint8
+    k, v = (torch.zeros(shape, dtype=dt, device=device) for _ in range(2))
+    ks, vs = (torch.zeros(num_pages, kv_heads, dtype=torch.float32, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs, head_dim)
+
+
+class KVBatch:
+    """The sequences of a call (wq_kv_batch): int32 ``cu_q`` [n_seqs + 1], ``seq_len`` [n_seqs] (tokens
+    of each sequence, those of the call included) and ``block_table`` [n_seqs, max_pages].  The tensors
+    may be rewritten in place between calls and between replays of a captured call."""
+
+    def __init__(self, cu_q, seq_len, block_table):
+        _same_device(cu_q.device, cu_q=cu_q, seq_len=seq_len, block_table=block_table)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [n_seqs, max_pages]")
+        n = block_table.shape[0]
+        _want(block_table, "block_table", torch.int32, block_table.shape)
+        _want(cu_q, "cu_q", torch.int32, (n + 1,))
+        _want(seq_len, "seq_len", torch.int32, (n,))
+        self.cu_q, self.seq_len, self.block_table, self.device = cu_q, seq_len, block_table, cu_q.device
+        self._c = _KVBatchC(cu_q.data_ptr(), seq_len.data_ptr(), block_table.data_ptr(), n, block_table.shape[1])
+
+
+def kv_append(qkv, cache: KVCache, batch: KVBatch, q_heads: int, rope=None, rope_style: int = ROPE_HALF, out=None,
+              stream=None) -> torch.Tensor:
+    """Rotate the queries and keys of ``qkv`` [M, (q_heads + 2 kv_heads) * head_dim] fp16/bf16 and append
+    its keys and values to ``cache``; returns the queries [M, q_heads, head_dim].
+
+    ``rope`` fp32 [positions, rope_dim]: cos, then sin, of the rope_dim / 2 angles of every position
+    (None: no rotation).  Each page and head keeps one scale, which grows (and re-codes the page's
+    earlier tokens) as larger values arrive."""
+    D = cache.head_dim
+    _same_device(cache.device, qkv=qkv, cu_q=batch.cu_q, rope=rope, out=out)
+    if qkv.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("qkv must be float16 or bfloat16")
+    if qkv.dim() != 2 or qkv.shape[1] != (q_heads + 2 * cache.kv_heads) * D:
+        raise ValueError(f"qkv must be [M, {(q_heads + 2 * cache.kv_heads) * D}], got {tuple(qkv.shape)}")
+    M = qkv.shape[0]
+    rope_len, rope_dim = 0, 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.dtype != torch.float32:
+            raise ValueError("rope must be float32 [positions, rope_dim]")
+        rope_len, rope_dim = rope.shape
+    with _Call(cache.device, stream) as s:
+        q = out if out is not None else torch.empty(M, q_heads, D, dtype=qkv.dtype, device=cache.device)
+        _want(q, "out", qkv.dtype, (M, q_heads, D))
+        rc = load_library().kv_append(_ptr(qkv), _DT[qkv.dtype], M, q_heads, _ptr(rope), rope_len, rope_dim,
+                                      rope_style, _ptr(q), cache._c, batch._c, s)
+    _check(rc, "kv_append")
+    return q
+
+
+def kv_attention_workspace_size(M: int, q_heads: int, cache: KVCache, batch: KVBatch) -> int:
+    with torch.cuda.device(cache.device):
+        return int(load_library().kv_attention_workspace_size(M, q_heads, cache._c, batch._c))
+
+
+def kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale: float | None = None, out=None, workspace=None,
+                 stream=None) -> torch.Tensor:
+    """Causal attention of ``q`` [M, q_heads, head_dim] fp16/bf16 over the cached keys and values of its
+    sequences (``sm_scale`` default head_dim ** -0.5); returns [M, q_heads, head_dim].
+
+    ``workspace``: :func:`make_workspace` of :func:`kv_attention_workspace_size` bytes, which lets few
+    rows over long contexts spread over the whole GPU."""
+    _same_device(cache.device, q=q, cu_q=batch.cu_q, out=out, workspace=workspace)
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16")
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [M, q_heads, {cache.head_dim}], got {tuple(q.shape)}")
+    M, q_heads, D = q.shape
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _Call(cache.device, stream) as s:
+        o = out if out is not None else torch.empty_like(q)
+        _want(o, "out", q.dtype, (M, q_heads, D))
+        rc = load_library().kv_attention(_ptr(q), _DT[q.dtype], M, q_heads, cache._c, batch._c,
+                                         D ** -0.5 if sm_scale is None else sm_scale, _ptr(o), _ptr(workspace), wsb, s)
+    _check(rc, "kv_attention")
+    return o
 
 
 def device_error() -> int:

@@ -29,6 +29,8 @@ wq_status tc_gemm(int WB, int AM, const void *A, const float *a_scale, const uin
                   const wq_qconfig &c, void *ws, size_t ws_bytes, cudaStream_t st);
 size_t tc_workspace_size(int64_t M, int64_t N, int64_t K);
 int tc_read_error();
+int kv_append_read_error();
+int kv_attn_read_error();
 
 namespace {
 thread_local char g_last_error[512] = "";
@@ -146,8 +148,11 @@ wq_status launch_prepared(PreparedLaunch &L, cudaStream_t st, const char *what)
 
 int read_device_errors()
 {
-    const int a = skinny_read_error(), b = gemv_read_error(), t = tc_read_error();
-    return a ? a : (b ? b : t);
+    int found = 0;  // every word is read and cleared
+    for (const int e : {skinny_read_error(), gemv_read_error(), tc_read_error(), kv_append_read_error(),
+                        kv_attn_read_error()})
+        found = found ? found : e;
+    return found;
 }
 
 namespace {

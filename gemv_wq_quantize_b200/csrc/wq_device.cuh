@@ -15,7 +15,7 @@ namespace wq {
 constexpr uint32_t kMaxPolls = 256;
 
 // Error codes recorded in the per-translation-unit device error word.
-enum : int { kErrNone = 0, kErrWaitTimeout = 1, kErrBadLaunch = 2 };
+enum : int { kErrNone = 0, kErrWaitTimeout = 1, kErrBadLaunch = 2, kErrRange = 3 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {

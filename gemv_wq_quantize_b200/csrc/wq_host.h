@@ -7,6 +7,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 
 #include "wq.h"
 #include "wq_format.h"
@@ -55,6 +56,19 @@ struct PreparedLaunch {
     alignas(64) unsigned char args[512];  // the kernel's arguments, each at its own offset
     void *argp[4] = {};                   // pointers into args, in parameter order
     int nargs = 0;
+    // A kernel with one argument structure.
+    template <typename A>
+    void set(const void *fn, dim3 g, dim3 b, size_t smem_bytes, const A &a)
+    {
+        static_assert(sizeof(A) <= sizeof args && alignof(A) <= 64, "argument structure");
+        func = fn;
+        grid = g;
+        block = b;
+        smem = smem_bytes;
+        memcpy(args, &a, sizeof a);
+        argp[0] = args;
+        nargs = 1;
+    }
     cudaKernelNodeParams node_params()
     {
         cudaKernelNodeParams k = {};
@@ -68,6 +82,9 @@ struct PreparedLaunch {
 };
 // Launches it on `st` with programmatic dependent launch allowed.
 wq_status launch_prepared(PreparedLaunch &L, cudaStream_t st, const char *what);
+
+// Checks of a cache and a batch of sequences (kv_append, kv_attention) on the host.
+wq_status check_kv(const wq_kv_cache *c, const wq_kv_batch *b, wq_dtype dt, int64_t M, int32_t q_heads);
 
 // Argument checks of w4a16_gemm (all but the workspace).
 wq_status check_a16(const void *A, wq_dtype a_dt, const uint8_t *Wq, const void *scales, const void *zeros,

@@ -1,0 +1,29 @@
+// wq_kv_attn.cuh -- arguments and entry points shared by the kernels of kv_attention.
+#pragma once
+#include <stdint.h>
+
+#include "wq_host.h"
+#include "wq_kv.h"
+
+namespace wq {
+
+struct KvAttnArgs {
+    const void *q;
+    void *out;
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    const int32_t *cu_q, *seq_len, *block_table;
+    int64_t num_pages;
+    int n_seqs, max_pages, M;
+    int q_heads, kv_heads, group, head_dim;
+    int page_shift, pitch, capacity;
+    float sm_scale;
+    float *partials;      // nullptr: every tile is walked by one block
+    unsigned *arrivals;
+};
+
+// Few rows per key head: split over the whole GPU by key ranges (wq_kv_attn.cu).
+wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st);
+size_t kv_attn_rows_workspace();
+
+}  // namespace wq

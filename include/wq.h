@@ -239,6 +239,111 @@ wq_status w8a8_fp8_gemm_fused(const void *A, wq_dtype a_dt, const uint8_t *Wq, c
                               const void *bias, void *C, uint8_t *Aq, float *a_scale, int64_t M, int64_t N,
                               int64_t K, wq_qconfig c, void *workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- The steps of a decoder layer between its matmuls: the norm in front of a projection, the
+ * append of keys and values behind the QKV projection, and attention over the cached keys and
+ * values.  They read and write what the matmuls above write and read: 16-bit rows, per-token
+ * 8-bit activations, and a key / value cache in the activations' two 8-bit formats.  (The
+ * survey pages name these steps as part of the serving stack around the matmul.) */
+
+/* RMS norm with the residual's addition, and its output quantized per token: the input that
+ * act_quant_int8 / act_quant_fp8 would otherwise read again.  For every token m:
+ *   h[m]       = X[m] + residual[m], rounded to dt (the new residual stream);
+ *                without a residual h[m] = X[m] and nothing is written to h
+ *   y[m,k]     = (h[m,k] * rstd[m]) * gamma[k], two binary32 products, with
+ *                rstd[m] = binary32(1 / sqrt(sum_k h[m,k]^2 / K + eps)), formed in binary64
+ *   a_scale[m] = max_k |y[m,k]| * r with r = binary32(1 / 127) (INT8) or binary32(1 / 448) (FP8)
+ *   Aq[m,k]    = the code of y / a_scale, as act_quant_int8 / act_quant_fp8 form it
+ *                (an all-zero token: scale 0, codes 0)
+ * A token whose y holds an infinity or NaN gets the scale NaN and codes 0, so that its products
+ * are NaN.  Bit-exact with any implementation of this text.
+ *   X, residual, h [M,K] and gamma [K] of type dt (WQ_F16 or WQ_BF16); residual and h are given
+ *   together or are both NULL; h may be X or residual.  Aq [M,K] codes and a_scale [M] written.
+ *   eps > 0 and finite; K % 8 == 0; M >= 1. */
+wq_status rmsnorm_quant_int8(const void *X, const void *residual, const void *gamma, wq_dtype dt, float eps,
+                             int64_t M, int64_t K, void *h, int8_t *Aq, float *a_scale, cudaStream_t stream);
+wq_status rmsnorm_quant_fp8(const void *X, const void *residual, const void *gamma, wq_dtype dt, float eps,
+                            int64_t M, int64_t K, void *h, uint8_t *Aq, float *a_scale, cudaStream_t stream);
+
+/* A key / value cache in 8 bits, in pages of page_size tokens, with one binary32 scale for each
+ * page and key head: the value of a code c is scale[page, head] * c (INT8 codes -127..127) or
+ * scale[page, head] * v(c) (e4m3; the codes 0x7f and 0xff, NaN, are not valid in a cache).
+ *   k, v              [num_pages, kv_heads, page_size, pitch] bytes, pitch = head_dim rounded up
+ *                     to a multiple of 16 (bytes head_dim .. pitch - 1 are neither written nor
+ *                     used)
+ *   k_scale, v_scale  [num_pages, kv_heads] binary32
+ * page_size 16, 32, 64, 128 or 256; head_dim a multiple of 4 from 16 to 256; kv_heads 1 to 1024;
+ * format WQ_FMT_INT (INT8) or WQ_FMT_E4M3.  k and v 16-byte aligned.  Nothing needs to be
+ * cleared before first use. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim, format;
+} wq_kv_cache;
+
+/* The sequences of a call (device arrays, so that a captured graph reads their values of each
+ * replay).  Sequence b owns the rows cu_q[b] .. cu_q[b+1] - 1 of the call's M token rows and,
+ * these included, has seq_len[b] tokens: its row i has position
+ *   p = seq_len[b] - (cu_q[b+1] - cu_q[b]) + i.
+ * Token p lives in page block_table[b, p / page_size], slot p % page_size.
+ *   cu_q [n_seqs + 1], seq_len [n_seqs], block_table [n_seqs, max_pages] int32; entries beyond a
+ *   sequence's last page are not read.  n_seqs 1 to 4096; max_pages * page_size < 2^31.
+ * A row with a negative position (an idle slot of a fixed-size batch: seq_len 0) has no place:
+ * kv_append stores nothing for it and kv_attention gives zeros.  Rows from cu_q[n_seqs] on are
+ * left as they were.  Sequences may share pages that they only read; a page that a call writes
+ * belongs to one sequence of the call.
+ * What the host cannot check is checked on the device: a needed block-table entry outside
+ * 0 .. num_pages - 1, or seq_len beyond max_pages * page_size or beyond the rope table, sets the
+ * device error word to 3 (wq_device_error); the tokens concerned are left out, nothing is
+ * accessed out of range, and results of those sequences are not valid.  cu_q is cut to 0..M. */
+typedef struct {
+    const int32_t *cu_q;
+    const int32_t *seq_len;
+    const int32_t *block_table;
+    int64_t n_seqs, max_pages;
+} wq_kv_batch;
+
+/* Rotates the queries and keys of a fused QKV projection's output by their positions, returns
+ * the queries and appends the keys and values to the cache.
+ *   qkv   [M, (q_heads + 2 kv_heads) * head_dim] of type dt (WQ_F16 or WQ_BF16): query heads,
+ *         key heads, value heads; q_heads a multiple of kv_heads.
+ *   rope  [rope_len, rope_dim] binary32: row p holds cos of the rope_dim / 2 angles of position
+ *         p, then their sin.  The first rope_dim values of each query and key head turn (even,
+ *         at most head_dim); the others pass.  WQ_ROPE_HALF pairs value i with i + rope_dim / 2,
+ *         WQ_ROPE_PAIRS 2i with 2i + 1:  (a, b) -> (a c - b s, b c + a s), every product and sum
+ *         rounded to binary32.  rope_dim 0 with rope NULL: no rotation.
+ *   q_out [M, q_heads * head_dim] of type dt, written (not part of qkv); rows without a place
+ *         are zeroed.
+ *   Cache scales, per page and key head (keys and values alike):
+ *     need  = max |x| * binary32(1 / 127 or 1 / 448) over the call's new tokens in the page
+ *     scale = max(scale before, need), or need where the page's slot 0 is among the new tokens
+ *   (so pages need no reset); where the scale grows, the codes of the page's earlier tokens
+ *   become the codes of value * (scale before / scale).  The codes of the new tokens are those
+ *   of x / scale (as act_quant_int8 / act_quant_fp8), from the rotated binary32 values.
+ *   Slots behind the new tokens are left as they were.  An infinite key or value is stored as
+ *   the largest code, NaN as 0, and neither counts for the scale, so that one bad token does not
+ *   reach its page's other tokens.
+ * Bit-exact with any implementation of this text.  M * q_heads < 2^31. */
+#define WQ_ROPE_HALF 0
+#define WQ_ROPE_PAIRS 1
+wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t q_heads, const float *rope, int64_t rope_len,
+                    int32_t rope_dim, int32_t rope_style, void *q_out, const wq_kv_cache *cache,
+                    const wq_kv_batch *batch, cudaStream_t stream);
+
+/* Causal attention of the call's rows over the cached keys and values of their sequences (the
+ * rows' own tokens included: append first):
+ *   out[m, h] = sum_{j <= p} softmax_j(sm_scale * q[m,h] . k_j) v_j,  key head h / (q_heads / kv_heads)
+ * with p the row's position; binary32 scores, softmax statistics and sums.
+ *   q, out [M, q_heads * head_dim] of type dt (WQ_F16 or WQ_BF16); sm_scale finite.
+ *   workspace: as for w4a16_gemm (kv_attention_workspace_size bytes, zero-filled once, shared by
+ *   calls that do not overlap); lets few rows over long contexts spread over the whole GPU.
+ *   NULL or too small: every key range is walked by one block.
+ * Results do not depend on timing: the same call on the same device gives the same bits. */
+wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t q_heads, const wq_kv_cache *cache,
+                       const wq_kv_batch *batch, float sm_scale, void *out, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream);
+size_t kv_attention_workspace_size(int64_t M, int32_t q_heads, const wq_kv_cache *cache, const wq_kv_batch *batch);
+
 /* Bytes of workspace that lets w4a16_gemm / w4a8_gemm use their split-K plans on the
  * current device (those of the tiled mma.sync path; 0 where that path is not used). */
 size_t wq_workspace_size(int64_t M, int64_t N, int64_t K, wq_qconfig c);
@@ -315,7 +420,8 @@ const char *wq_status_string(wq_status s);
 /* Reads and clears the library's device-side error word.  Non-zero means that a kernel's
  * outputs are not valid: 1, it gave up a bounded wait on one of its own barriers (about
  * 2 s) and returned early; 2, it found itself launched in another thread-block cluster
- * shape than planned and did no work.  Synchronous (device-to-host copy of one word); for
+ * shape than planned and did no work; 3, a key / value cache call met a page number or a
+ * position out of range and left those tokens out.  Synchronous (device-to-host copy of one word); for
  * tests and diagnostics. */
 int wq_device_error(void);
 /* One-line reason for the last non-OK status returned on the calling thread. */
