@@ -92,6 +92,24 @@ __device__ __forceinline__ float code_value(uint32_t w, int i)
     }
 }
 
+// binary16 pair of two 8-bit codes: bytes HALF * 2 and HALF * 2 + 1 of w.  INT8 comes with its
+// sign bits flipped (c + 128 in 0..255): 0x6400 | byte is 1024 + byte, less 1152.
+template <bool F8, int HALF>
+__device__ __forceinline__ uint32_t widen(uint32_t w)
+{
+    if constexpr (F8) return e4m3x2_to_f16x2<HALF>(w);
+    else return h2_add(prmt(w, 0x64646464u, HALF ? 0x4342 : 0x4140), 0xE480E480u);
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 __device__ __forceinline__ uint32_t warp_umax(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 }  // namespace wq

@@ -31,6 +31,7 @@ size_t tc_workspace_size(int64_t M, int64_t N, int64_t K);
 int tc_read_error();
 int kv_append_read_error();
 int kv_attn_read_error();
+int kv_tiles_read_error();
 
 namespace {
 thread_local char g_last_error[512] = "";
@@ -150,7 +151,7 @@ int read_device_errors()
 {
     int found = 0;  // every word is read and cleared
     for (const int e : {skinny_read_error(), gemv_read_error(), tc_read_error(), kv_append_read_error(),
-                        kv_attn_read_error()})
+                        kv_attn_read_error(), kv_tiles_read_error()})
         found = found ? found : e;
     return found;
 }

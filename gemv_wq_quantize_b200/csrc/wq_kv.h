@@ -86,6 +86,11 @@ WQ_HD int64_t kv_scale_index(int64_t page, int head, int heads) { return page * 
 WQ_HD int64_t kv_tiles(int n, int group, int rows) { return (int64_t(n) * group + rows - 1) / rows; }
 WQ_HD int64_t kv_units(int len, int unit) { return len > 0 ? (int64_t(len) + unit - 1) / unit : 1; }
 
+// Blocks of `rows` rows for the sequences of a call without a sum over them: sequence b owns
+// the items from kv_row_item(q0_b, b) to kv_row_item(q0_{b+1}, b + 1), at least
+// floor(n * group / rows) + 1 >= kv_tiles(n, group, rows) of them.
+WQ_HD int64_t kv_row_item(int q0, int b, int group, int rows) { return int64_t(q0) * group / rows + b; }
+
 // Units [lo, hi) of the `total` that block `c` of `grid` takes.
 WQ_HD int64_t kv_share(int64_t total, int c, int grid) { return total / grid * c + total % grid * c / grid; }
 

@@ -46,20 +46,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 64;  // keys of a unit: the granule of the split
 
-constexpr float kLog2e = 1.4426950408889634f;
 // exp2 arguments are raised by 15: the weights then reach 2^15 in binary16 (its largest is just
 // below 2^16) and keep full precision down to 2^-29 of the largest weight, so that many small
 // weights under one large one are not lost; the sum carries the same factor.
 constexpr float kRaise = 15.f;
-
-// binary16 pair of two 8-bit codes: bytes HALF * 2 and HALF * 2 + 1 of w.  INT8 comes with its
-// sign bits flipped (c + 128 in 0..255): 0x6400 | byte is 1024 + byte, less 1152.
-template <bool F8, int HALF>
-__device__ __forceinline__ uint32_t widen(uint32_t w)
-{
-    if constexpr (F8) return e4m3x2_to_f16x2<HALF>(w);
-    else return h2_add(prmt(w, 0x64646464u, HALF ? 0x4342 : 0x4140), 0xE480E480u);
-}
 
 __device__ __forceinline__ uint32_t trans8x8(uint32_t x)
 {
@@ -81,13 +71,6 @@ __device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p)
     uint2 v;
     asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
-}
-
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // DT: head_dim rounded up to 64, 128 or 256.  NT: tiles of 8 rows.
@@ -457,6 +440,7 @@ kv_attn_rows_kernel(const __grid_constant__ KvAttnArgs a)
         const int len = a.seq_len[b];
         const KvSpan s = kv_span(a.cu_q[b], a.cu_q[b + 1], len, a.M, a.capacity);
         if (len > a.capacity) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
+        if (int64_t(s.n) * a.group > a.few_rows) return int64_t(0);
         return kv_tiles(s.n, a.group, S::kRows) * (split ? kv_units(s.len, kUnit) : 1) * a.kv_heads;
     };
     int64_t mine = 0;
@@ -648,6 +632,7 @@ RowsPlan rows_plan(int head_dim, bool two)
 }
 
 constexpr int kMostPerSm = 3;
+constexpr int kFewRows = 16;
 // two partial slots a block: the largest of 3 blocks of 8 rows of 130 binary32 values, 2 blocks
 // of 16 rows of 258
 static_assert(3 * 2 * 8 * (128 + 2) * 4 <= 65536 && 2 * 2 * 16 * (256 + 2) * 4 <= 2 * 65536, "");
@@ -725,5 +710,12 @@ extern "C" wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t
         a.arrivals = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) +
                                                   std::max(rows_partial_bytes(), ws_scratch_bytes()));
     }
-    return kv_attn_rows(a, dt == WQ_BF16, cache->format == WQ_FMT_E4M3, stream);
+    // Sequences with up to kFewRows rows per key head are bound by reading their keys once and go
+    // to the key-split kernel, the others to the tile kernel (heads up to 128).  One launch
+    // where sequences bring that few rows on average, right for any distribution.
+    const bool bf16 = dt == WQ_BF16, f8 = cache->format == WQ_FMT_E4M3;
+    const bool tiles = a.head_dim <= 128 && M * a.group > kFewRows * batch->n_seqs;
+    a.few_rows = tiles ? kFewRows : 0x7fffffff;
+    rc = kv_attn_rows(a, bf16, f8, stream);
+    return rc == WQ_OK && tiles ? kv_attn_tiles(a, bf16, f8, stream) : rc;
 }

@@ -18,6 +18,7 @@ struct KvAttnArgs {
     int q_heads, kv_heads, group, head_dim;
     int page_shift, pitch, capacity;
     float sm_scale;
+    int few_rows;         // sequences with more rows per key head go to the tile kernel
     float *partials;      // nullptr: every tile is walked by one block
     unsigned *arrivals;
 };
@@ -25,5 +26,8 @@ struct KvAttnArgs {
 // Few rows per key head: split over the whole GPU by key ranges (wq_kv_attn.cu).
 wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st);
 size_t kv_attn_rows_workspace();
+
+// Many rows per key head (prefill): 256-row tiles on the tensor cores (wq_kv_tiles.cu).
+wq_status kv_attn_tiles(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st);
 
 }  // namespace wq

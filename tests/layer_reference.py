@@ -141,13 +141,14 @@ def append_bits(qkv, cache, cu_q, seq_len, table, q_heads, kv_heads, rope, style
 
 
 def attention_64(q, cache, cu_q, seq_len, table, sm_scale, num_pages):
-    """(out, mass, score, plain, own): the attention in 64 bits, and for every output the terms its
-    error bound is made of: sum w |v|, the largest error of a score in units of 2^-24, and sum |v|.
+    """(out, mass, score, plain, top, own): the attention in 64 bits, and for every output the terms its
+    error bound is made of: sum w |v|, the largest error of a score in units of 2^-24, sum |v|, and
+    the sum of |codes| times the largest value scale.
     own: the rows that belong to a sequence.  Tokens whose block-table entry is no page are left
     out."""
     M, Hq, D = q.shape
     Hkv, ps = cache.k.shape[1], cache.page
-    out, mass, plain, score = (np.zeros((M, Hq, d)) for d in (D, D, D, 1))
+    out, mass, plain, top, score = (np.zeros((M, Hq, d)) for d in (D, D, D, D, 1))
     own = np.zeros(M, bool)
     for b in range(len(seq_len)):
         n, ln = cu_q[b + 1] - cu_q[b], seq_len[b]
@@ -160,7 +161,8 @@ def attention_64(q, cache, cu_q, seq_len, table, sm_scale, num_pages):
         pg = np.where(fine, pages, 0)
         for h in range(Hkv):
             k = values_of(cache.k[pg, h, at % ps, :D], cache.out) * cache.ks[pg, h].astype(np.float64)[:, None]
-            v = values_of(cache.v[pg, h, at % ps, :D], cache.out) * cache.vs[pg, h].astype(np.float64)[:, None]
+            vc, vs = values_of(cache.v[pg, h, at % ps, :D], cache.out), cache.vs[pg, h].astype(np.float64)
+            v = vc * vs[:, None]
             G = Hq // Hkv
             for i in range(n):
                 see = np.flatnonzero((at <= ln - n + i) & fine)
@@ -174,7 +176,8 @@ def attention_64(q, cache, cu_q, seq_len, table, sm_scale, num_pages):
                 out[rows] = w @ v[see]
                 mass[rows] = w @ np.abs(v[see])
                 plain[rows] = np.abs(v[see]).sum(0)
+                top[rows] = np.abs(vc[see]).sum(0) * vs[see].max()
                 # D products and sums; the queries' 16-bit form: 2^-25 of the largest, per term
                 err = (D + 16) * (np.abs(qs) @ np.abs(k[see]).T) + np.abs(qs).max(1, keepdims=True) * np.abs(k[see]).sum(1)
                 score[rows] = (err * abs(sm_scale)).max(1, keepdims=True)
-    return out, mass, score, plain, own
+    return out, mass, score, plain, top, own

@@ -337,13 +337,19 @@ def _attend(s, q, cache, batch, workspace=True, **kw):
     return wq.kv_attention(_dev(q, s.dt), cache, batch, out=out, workspace=ws, **kw)
 
 
-def _attend_check(s, q, got, sm_scale=None):
+def _attend_check(s, q, got, sm_scale=None, tiles=False):
     sm = s.D ** -0.5 if sm_scale is None else sm_scale
-    want, mass, score, plain, own = ref.attention_64(q, s.host, s.cu, s.total, s.table, float(np.float32(sm)), s.num_pages)
+    want, mass, score, plain, top, own = ref.attention_64(q, s.host, s.cu, s.total, s.table, float(np.float32(sm)), s.num_pages)
     g = _np(got)
     assert (g[~own] == MARK).all()
     off = np.abs(g - want)[own]
-    lim = _bound(want, mass, score, plain, max(s.total), s.dtype)[own]
+    lim = _bound(want, mass, score, plain, max(s.total), s.dtype)
+    if tiles:
+        # many rows: a weight enters binary16 as 2^11 times its share of a reference that is at most
+        # the largest weight, times its value scale over a power of two that is at most twice the
+        # largest: half a step, 2^-25, is 2^-25 / 2^11 * 2 = 2^-35 of the largest scale
+        lim = lim + 2.0 ** -35 * top
+    lim = lim[own]
     assert np.isfinite(g[own]).all()
     assert (off <= lim).all(), f"worst {np.max(off / np.maximum(lim, 1e-300))} of the bound"
 
@@ -413,6 +419,54 @@ def test_attention_scores_of_any_size():
         q = ref.to_t(s.q() * size, torch.bfloat16)
         cache, batch = s.device()
         _attend_check(s, q, _attend(s, q, cache, batch, sm_scale=sm), sm)
+
+
+TILES = [
+    ([300], [300], 4, 2, 128, 16),                             # three blocks of 256 rows, causal
+    ([200, 3, 129], [900, 200, 129], 4, 2, 128, 64),           # long past; a sequence of few rows among them
+    ([256, 128, 1, 0, 57], [256, 640, 5, 90, 57], 1, 1, 128, 32),
+    ([140, 60], [100, 60], 2, 1, 64, 128),                     # rows before the first key
+    ([90, 45], [333, 45], 5, 1, 100, 32),
+    ([70], [1500], 8, 1, 48, 256),
+    ([100, 100], [100, 0], 3, 3, 112, 16),                     # all rows without keys
+]
+
+
+@pytest.mark.parametrize("dtype,out", [("fp16", "int8"), ("fp16", "fp8"), ("bf16", "int8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("case", TILES, ids=lambda c: "q%s_h%d-%d_d%d_p%d" % ("-".join(map(str, c[0])), c[2], c[3], c[4], c[5]))
+def test_attention_many_rows(case, dtype, out):
+    new, total, hq, hkv, D, page = case
+    s = Setup(new, total, hq, hkv, D, page, dtype, out, seed=sum(total) + D, tail=3).fill(total)
+    cache, batch = s.device()
+    q = s.q()
+    got = _attend(s, q, cache, batch)
+    _attend_check(s, q, got, tiles=True)
+    assert torch.equal(_attend(s, q, cache, batch), got)
+
+
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+def test_attention_many_rows_uneven(out):
+    """Value scales and scores that rise by orders of magnitude along the keys and fall again: the running
+    references move often."""
+    s = Setup([150], [700], 2, 1, 128, 16, "fp16", out, seed=31).fill([700])
+    order = s.table[0, : -(-700 // 16)]
+    rise = np.concatenate([np.linspace(-4, 0, 30), np.linspace(0, -5, order.size - 30)])
+    s.host.vs[order, 0] = (10.0 ** rise * 0.03).astype(np.float32)
+    s.host.ks[order, 0] = (s.host.ks[order, 0] * 10.0 ** np.linspace(-2, 0.8, order.size)).astype(np.float32)
+    q = s.q()
+    cache, batch = s.device()
+    _attend_check(s, q, _attend(s, q, cache, batch), tiles=True)
+
+
+def test_attention_many_rows_with_a_bad_page():
+    s = Setup([60, 60], [300, 300], 2, 1, 128, 16, "bf16", "fp8", seed=33).fill([300, 300])
+    s.table[0, 4] = -7
+    cache, batch = s.device()
+    q = s.q()
+    got = _attend(s, q, cache, batch)
+    torch.cuda.synchronize()
+    assert wq.device_error() == 3
+    _attend_check(s, q, got, tiles=True)
 
 
 def test_attention_many_sequences():

@@ -29,6 +29,7 @@ long long code_offset(long long p, int h, int s, int H, int sh, int pitch) { ret
 long long scale_index(long long p, int h, int H) { return kv_scale_index(p, h, H); }
 long long tiles(int n, int g, int r) { return kv_tiles(n, g, r); }
 long long units(int len, int u) { return kv_units(len, u); }
+long long row_item(int q0, int b, int g, int r) { return kv_row_item(q0, b, g, r); }
 long long share(long long t, int c, int g) { return kv_share(t, c, g); }
 }
 """
@@ -42,7 +43,7 @@ def kv(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "gemv_wq_quantize_b200", "csrc"), str(d / "kv.cpp"), "-o", str(so)], check=True)
     lib = ctypes.CDLL(str(so))
-    for f in ("item_start", "page_ok", "code_offset", "scale_index", "tiles", "units", "share"):
+    for f in ("item_start", "page_ok", "code_offset", "scale_index", "tiles", "units", "share", "row_item"):
         getattr(lib, f).restype = ctypes.c_longlong
     for f, t in (("page_ok", [ctypes.c_int, ctypes.c_longlong]), ("share", [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]),
                  ("code_offset", [ctypes.c_longlong] + [ctypes.c_int] * 5), ("scale_index", [ctypes.c_longlong] + [ctypes.c_int] * 2),
@@ -102,6 +103,15 @@ def test_item_starts_never_overlap(kv):
         starts = [kv.item_start(int(q), b, shift) for b, q in enumerate(cu)]
         assert all(b - a >= 2 for a, b in zip(starts, starts[1:]))
         assert starts[-1] <= (int(cu[-1]) >> shift) + 2 * 50
+
+
+def test_row_blocks_of_sequences_never_overlap(kv):
+    r = np.random.default_rng(1)
+    for group, rows in ((1, 256), (5, 256), (8, 256), (3, 16)):
+        cu = np.concatenate([[0], np.cumsum(r.integers(0, 700, 40))])
+        for b, (lo, hi) in enumerate(zip(cu, cu[1:])):
+            first, end = kv.row_item(int(lo), b, group, rows), kv.row_item(int(hi), b + 1, group, rows)
+            assert end - first >= kv.tiles(int(hi - lo), group, rows)
 
 
 def test_pages_offsets_and_shares(kv):
