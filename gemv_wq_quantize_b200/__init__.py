@@ -420,69 +420,83 @@ def w4a8_gemm_fused(A, Wq, scales, zeros, N: int, K: int, qc: QuantConfig, bias=
 # ---------------------------------------------------------------- a layer's steps between its matmuls
 def _same_device(device, **tensors):
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, other arguments are on {device}")
-        if not t.is_contiguous():
+        if t is not None and not (t.is_cuda and t.device == device and t.is_contiguous()):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, other arguments are on {device}")
             raise ValueError(f"{name} must be contiguous")
 
 
 def _want(t, name, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-class _Call:
-    """The tensors' device made current, and a stream of that device (the given one or its current
-    one).  Outputs are made on that stream, so that the allocator orders their reuse by it."""
+def _stream_of(device, stream):
+    """(raw stream, guard): the given stream, or the current one of the tensors' device.  The guard
+    (None where nothing has to change) makes the device and the stream current, so that launches go to
+    the device and outputs are made on the stream that writes them: the allocator orders their reuse
+    by it."""
+    if stream is None:
+        # (torch.cuda.current_stream() takes several microseconds, most of a small call)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        return raw, None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
-    def __init__(self, device, stream):
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors are on {device}")
-        self._guard = None
-        if torch.cuda.current_device() != device.index or stream is not None:
-            self._guard = torch.cuda.stream(self.stream)  # also makes the stream's device current
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+def _guarded(f):
+    """Runs f(raw stream) under the guard of _stream_of."""
+    def call(device, stream, *args):
+        raw, guard = _stream_of(device, stream)
+        if guard is None:
+            return f(raw, *args)
+        with guard:
+            return f(raw, *args)
+    return call
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _ip(t):
+    """The device pointer as the integer that a c_void_p argument takes (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+@_guarded
+def _rmsnorm_call(raw, name, code_dtype, X, gamma, eps, residual, out_residual, out_q, out_scale):
+    M, K = X.shape
+    h = out_residual if out_residual is not None or residual is None else torch.empty_like(X)
+    q = out_q if out_q is not None else torch.empty_like(X, dtype=code_dtype)
+    sc = out_scale if out_scale is not None else torch.empty(M, dtype=torch.float32, device=X.device)
+    rc = getattr(_lib or load_library(), name)(X.data_ptr(), _ip(residual), gamma.data_ptr(), _DT[X.dtype], eps, M, K,
+                                               _ip(h), q.data_ptr(), sc.data_ptr(), raw)
+    if rc:
+        _check(rc, name)
+    return q, sc, h
 
 
 def _rmsnorm_quant(name, code_dtype, X, gamma, eps, residual, out_residual, out_q, out_scale, stream):
     if X.dim() != 2:
         raise ValueError("X must be [M, K]")
-    if X.dtype not in (torch.float16, torch.bfloat16):
+    dt = X.dtype
+    if dt is not torch.float16 and dt is not torch.bfloat16:
         raise ValueError("X must be float16 or bfloat16")
     _same_device(X.device, X=X, gamma=gamma, residual=residual, out_residual=out_residual, out_q=out_q,
                  out_scale=out_scale)
     M, K = X.shape
-    _want(gamma, "gamma", X.dtype, (K,))
+    _want(gamma, "gamma", dt, (K,))
     if residual is not None:
-        _want(residual, "residual", X.dtype, (M, K))
-    elif out_residual is not None:
-        raise ValueError("out_residual needs residual")
-    with _Call(X.device, stream) as s:
-        h = None
-        if residual is not None:
-            h = out_residual if out_residual is not None else torch.empty_like(X)
-            _want(h, "out_residual", X.dtype, (M, K))
-        q = out_q if out_q is not None else torch.empty(M, K, dtype=code_dtype, device=X.device)
-        sc = out_scale if out_scale is not None else torch.empty(M, dtype=torch.float32, device=X.device)
-        _want(q, "out_q", code_dtype, (M, K))
-        _want(sc, "out_scale", torch.float32, (M,))
-        rc = getattr(load_library(), name)(_ptr(X), _ptr(residual), _ptr(gamma), _DT[X.dtype], eps, M, K, _ptr(h),
-                                           _ptr(q), _ptr(sc), s)
-    _check(rc, name)
-    return q, sc, h
+        _want(residual, "residual", dt, (M, K))
+    if out_residual is not None:
+        if residual is None:
+            raise ValueError("out_residual needs residual")
+        _want(out_residual, "out_residual", dt, (M, K))
+    if out_q is not None:
+        _want(out_q, "out_q", code_dtype, (M, K))
+    if out_scale is not None:
+        _want(out_scale, "out_scale", torch.float32, (M,))
+    return _rmsnorm_call(X.device, stream, name, code_dtype, X, gamma, eps, residual, out_residual, out_q, out_scale)
 
 
 def rmsnorm_quant_int8(X, gamma, eps: float, residual=None, out_residual=None, out_q=None, out_scale=None,
@@ -571,12 +585,19 @@ def kv_append(qkv, cache: KVCache, batch: KVBatch, q_heads: int, rope=None, rope
         if rope.dim() != 2 or rope.dtype != torch.float32:
             raise ValueError("rope must be float32 [positions, rope_dim]")
         rope_len, rope_dim = rope.shape
-    with _Call(cache.device, stream) as s:
-        q = out if out is not None else torch.empty(M, q_heads, D, dtype=qkv.dtype, device=cache.device)
-        _want(q, "out", qkv.dtype, (M, q_heads, D))
-        rc = load_library().kv_append(_ptr(qkv), _DT[qkv.dtype], M, q_heads, _ptr(rope), rope_len, rope_dim,
-                                      rope_style, _ptr(q), cache._c, batch._c, s)
-    _check(rc, "kv_append")
+    if out is not None:
+        _want(out, "out", qkv.dtype, (M, q_heads, D))
+    return _append_call(cache.device, stream, qkv, cache, batch, q_heads, rope, rope_len, rope_dim, rope_style, out)
+
+
+@_guarded
+def _append_call(raw, qkv, cache, batch, q_heads, rope, rope_len, rope_dim, rope_style, out):
+    M = qkv.shape[0]
+    q = out if out is not None else torch.empty((M, q_heads, cache.head_dim), dtype=qkv.dtype, device=qkv.device)
+    rc = (_lib or load_library()).kv_append(qkv.data_ptr(), _DT[qkv.dtype], M, q_heads, _ip(rope), rope_len, rope_dim,
+                                            rope_style, q.data_ptr(), cache._c, batch._c, raw)
+    if rc:
+        _check(rc, "kv_append")
     return q
 
 
@@ -599,12 +620,19 @@ def kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale: float | None = Non
         raise ValueError(f"q must be [M, q_heads, {cache.head_dim}], got {tuple(q.shape)}")
     M, q_heads, D = q.shape
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _Call(cache.device, stream) as s:
-        o = out if out is not None else torch.empty_like(q)
-        _want(o, "out", q.dtype, (M, q_heads, D))
-        rc = load_library().kv_attention(_ptr(q), _DT[q.dtype], M, q_heads, cache._c, batch._c,
-                                         D ** -0.5 if sm_scale is None else sm_scale, _ptr(o), _ptr(workspace), wsb, s)
-    _check(rc, "kv_attention")
+    if out is not None:
+        _want(out, "out", q.dtype, q.shape)
+    return _attention_call(cache.device, stream, q, cache, batch, D ** -0.5 if sm_scale is None else sm_scale, out,
+                           workspace, wsb)
+
+
+@_guarded
+def _attention_call(raw, q, cache, batch, sm_scale, out, workspace, wsb):
+    o = out if out is not None else torch.empty_like(q)
+    rc = (_lib or load_library()).kv_attention(q.data_ptr(), _DT[q.dtype], q.shape[0], q.shape[1], cache._c, batch._c,
+                                               sm_scale, o.data_ptr(), _ip(workspace), wsb, raw)
+    if rc:
+        _check(rc, "kv_attention")
     return o
 
 

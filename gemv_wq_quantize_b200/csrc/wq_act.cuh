@@ -42,40 +42,64 @@ __device__ __forceinline__ uint32_t act_t2(float a, float b)
 template <bool F8>
 constexpr float kInvQmax = F8 ? 1.f / 448.f : 1.f / 127.f;
 
-// INT8 code of a finite v for the scale s > 0: clip(rint(v / s), -127, 127) with the IEEE
-// quotient.  quant_i8 forms it from the reciprocal r of s (with a division next to ties
-// only); a scale at or below 2^-128 has no finite reciprocal and divides.
-__device__ __forceinline__ int code_i8(float v, float s, float r)
+// 8-bit codes of v / s (the IEEE quotient, then nearest, ties to even) without a division per
+// value: with r = 1 / s correctly rounded, v r (1 - 2^-21) and v r (1 + 2^-21) enclose v / s (r,
+// its factor and the products are off by 2^-24 each), and rounding to codes is monotone, so where
+// both give the same code it is the quotient's.  Only four values of which one lies that near to a
+// border between codes are divided.
+struct CodeScale {
+    float s, lo, hi;
+    bool divide;  // a scale whose reciprocal is not a normal number
+};
+__device__ __forceinline__ CodeScale code_scale(float s)
 {
-    if (isinf(r)) return int(fminf(fmaxf(rintf(__fdiv_rn(v, s)), -127.f), 127.f));
-    return quant_i8(v, s, r);
+    const float r = s != 0.f ? __frcp_rn(s) : 0.f;
+    return {s, __fmul_rn(r, 1.f - 0x1p-21f), __fmul_rn(r, 1.f + 0x1p-21f), s != 0.f && !(s >= 0x1p-126f && s <= 0x1p126f)};
 }
 
-// Four e4m3 codes of a, b, c, d (already divided by their scale): nearest, ties to even,
-// values beyond 448 saturate, a zero result is +0 (the convention of act_quant_fp8).
-__device__ __forceinline__ uint32_t codes_e4m3(float a, float b, float c, float d)
+// Four e4m3 codes: nearest, ties to even, values beyond 448 saturate, a zero result is +0 (the
+// convention of act_quant_fp8).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t w = lo | (hi << 16);
+    return lo | (hi << 16);
+}
+__device__ __forceinline__ uint32_t e4m3_plus_zero(uint32_t w)
+{
     const uint32_t nonzero = (w & 0x7f7f7f7fu) + 0x7f7f7f7fu;  // bit 7 of a byte: its magnitude is not 0
     return w & (nonzero | 0x7f7f7f7fu);
 }
 
-// Four codes of finite values for one scale s >= 0 with reciprocal r (INT8; unused for
-// e4m3, whose quotients are IEEE divisions): 0 where s is 0.
-template <bool F8>
-__device__ __forceinline__ uint32_t codes4(const float (&v)[4], float s, float r)
+// Four INT8 codes of v * r for |v * r| < 128: 1.5 * 2^23 + v r leaves the nearest integer in the
+// low byte of the sum's pattern.
+__device__ __forceinline__ uint32_t i8x4(const float (&v)[4], float r)
 {
-    if (s == 0.f) return 0u;
-    if constexpr (F8) {
-        return codes_e4m3(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s), __fdiv_rn(v[2], s), __fdiv_rn(v[3], s));
-    } else {
-        uint32_t w = 0;
+    uint32_t b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w |= (uint32_t(code_i8(v[i], s, r)) & 0xffu) << (8 * i);
-        return w;
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fmaf_rn(v[i], r, 12582912.f));
+    return prmt(prmt(b[0], b[1], 0x0040), prmt(b[2], b[3], 0x0040), 0x5410);
+}
+
+// Codes of four values with |v| <= qmax * s up to rounding (0 where s is 0).
+template <bool F8>
+__device__ __forceinline__ uint32_t codes4(const float (&v)[4], const CodeScale &c)
+{
+    uint32_t lo, hi;
+    if constexpr (F8) {
+        lo = e4m3x4(v[0] * c.lo, v[1] * c.lo, v[2] * c.lo, v[3] * c.lo);
+        hi = e4m3x4(v[0] * c.hi, v[1] * c.hi, v[2] * c.hi, v[3] * c.hi);
+    } else {
+        lo = i8x4(v, c.lo);
+        hi = i8x4(v, c.hi);
     }
+    if (lo != hi || c.divide) {
+        float q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = fminf(fmaxf(__fdiv_rn(v[i], c.s), F8 ? -448.f : -127.f), F8 ? 448.f : 127.f);
+        lo = F8 ? e4m3x4(q[0], q[1], q[2], q[3]) : i8x4(q, 1.f);
+    }
+    return F8 ? e4m3_plus_zero(lo) : lo;
 }
 
 // The value of code i (byte i of w).

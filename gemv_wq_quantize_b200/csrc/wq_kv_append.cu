@@ -40,7 +40,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeldFloats = 64;  // binary32 values of a page that a lane keeps in registers
+constexpr int kHeldFloats = 32;  // binary32 values of a page that a lane keeps in registers
+
+// How the values of a row turn: kPairs: partners among a lane's four values, cos / sin in aligned
+// pairs; kHalf: partners rope_dim / 2 away, everything 8-byte aligned; kAny: neither (a rope_dim
+// that is no multiple of 4 or 8); kNone.
+enum Mode { kNone, kPairs, kHalf, kAny };
 
 struct AppendArgs {
     const void *qkv;
@@ -54,94 +59,237 @@ struct AppendArgs {
     int capacity;       // tokens that the block table's row holds
     int limit;          // positions below it have a place: min(capacity, rope_len)
     bool pairs;         // WQ_ROPE_PAIRS
-    bool vec;           // four neighbouring values turn alike and their partners are 8-byte aligned
     int64_t kv_items;   // (sequence, page) items
-    int head_blocks;    // blocks per item
+    int parts;          // blocks per item
     int q_tokens;       // tokens of a query block
 };
 
-// Four neighbouring values d .. d + 3 of one head row, rotated by the position whose table row
-// is `tab` (nullptr: not rotated).
-template <typename T>
-__device__ __forceinline__ void load_turned(const AppendArgs &a, const T *row, int d, const float *tab, float (&y)[4])
+// Four neighbouring values d .. d + 3 of a head row and their rotation.  Loads and arithmetic are
+// apart, and the loads of a row that does not turn (or of a lane behind the head) go to a valid
+// address and are not used: without branches around them the loads of many rows are in flight
+// before the first is worked on.
+struct Turn {
+    float c[4], s[4];
+};
+struct Raw {
+    uint2 x, p;  // the values and (kHalf) their partners
+};
+
+template <Mode MODE>
+__device__ __forceinline__ Turn load_turn(const AppendArgs &a, const float *tab, int d)
 {
-    const uint2 raw = *reinterpret_cast<const uint2 *>(row + d);
-    const float2 lo = act_f2<T>(raw.x), hi = act_f2<T>(raw.y);
-    const float x[4] = {lo.x, lo.y, hi.x, hi.y};
-    const int r = a.rope_dim, half = r / 2;
-    if (tab == nullptr || d >= r) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = x[i];
-    } else if (a.vec && a.pairs) {
-        const float2 c = *reinterpret_cast<const float2 *>(tab + d / 2);
-        const float2 s = *reinterpret_cast<const float2 *>(tab + half + d / 2);
-        y[0] = __fsub_rn(__fmul_rn(x[0], c.x), __fmul_rn(x[1], s.x));
-        y[1] = __fadd_rn(__fmul_rn(x[1], c.x), __fmul_rn(x[0], s.x));
-        y[2] = __fsub_rn(__fmul_rn(x[2], c.y), __fmul_rn(x[3], s.y));
-        y[3] = __fadd_rn(__fmul_rn(x[3], c.y), __fmul_rn(x[2], s.y));
-    } else if (a.vec) {
-        const bool first = d < half;
-        const int u = first ? d : d - half;
-        const uint2 praw = *reinterpret_cast<const uint2 *>(row + (first ? d + half : d - half));
-        const float2 plo = act_f2<T>(praw.x), phi = act_f2<T>(praw.y);
-        const float p[4] = {plo.x, plo.y, phi.x, phi.y};
-        const float4 c = *reinterpret_cast<const float4 *>(tab + u);
-        const float4 s = *reinterpret_cast<const float4 *>(tab + half + u);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    Turn t{};
+    const int half = a.rope_dim / 2;
+    if constexpr (MODE == kPairs) {
+        const int u = d < a.rope_dim ? d / 2 : 0;
+        const float2 c = __ldg(reinterpret_cast<const float2 *>(tab + u));
+        const float2 s = __ldg(reinterpret_cast<const float2 *>(tab + half + u));
+        t.c[0] = t.c[1] = c.x;
+        t.c[2] = t.c[3] = c.y;
+        t.s[0] = t.s[1] = s.x;
+        t.s[2] = t.s[3] = s.y;
+    } else if constexpr (MODE == kHalf) {
+        const int u = d < half ? d : (d < a.rope_dim ? d - half : 0);
+        const float4 c = __ldg(reinterpret_cast<const float4 *>(tab + u));
+        const float4 s = __ldg(reinterpret_cast<const float4 *>(tab + half + u));
+        t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
+        t.s[0] = s.x; t.s[1] = s.y; t.s[2] = s.z; t.s[3] = s.w;
+    } else if constexpr (MODE == kAny) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float xc = __fmul_rn(x[i], cc[i]), ps = __fmul_rn(p[i], ss[i]);
-            y[i] = first ? __fsub_rn(xc, ps) : __fadd_rn(xc, ps);
+            const int e = min(d + i, a.rope_dim - 1);
+            const int u = a.pairs ? e / 2 : (e < half ? e : e - half);
+            t.c[i] = __ldg(tab + u);
+            t.s[i] = __ldg(tab + half + u);
         }
-    } else {
+    }
+    return t;
+}
+
+template <typename T, Mode MODE>
+__device__ __forceinline__ Raw load_raw(const AppendArgs &a, const T *row, int d)
+{
+    Raw r;
+    r.x = __ldg(reinterpret_cast<const uint2 *>(row + d));
+    if constexpr (MODE == kHalf) {
+        const int half = a.rope_dim / 2;
+        r.p = __ldg(reinterpret_cast<const uint2 *>(row + (d < half ? d + half : (d < a.rope_dim ? d - half : d))));
+    } else if constexpr (MODE == kAny) {
+        const uint16_t *w = reinterpret_cast<const uint16_t *>(row);
+        const int half = a.rope_dim / 2;
+        uint16_t p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            const int e = min(d + i, a.rope_dim - 1);
+            p[i] = __ldg(w + (a.pairs ? (e ^ 1) : (e < half ? e + half : e - half)));
+        }
+        r.p = make_uint2(p[0] | uint32_t(p[1]) << 16, p[2] | uint32_t(p[3]) << 16);
+    }
+    return r;
+}
+
+// A value x with partner p turns to x c - p s (first of its pair) or x c + p s (second).
+template <typename T, Mode MODE>
+__device__ __forceinline__ void turn4(const AppendArgs &a, int d, const Raw &r, const Turn &t, float (&y)[4])
+{
+    const float2 lo = act_f2<T>(r.x.x), hi = act_f2<T>(r.x.y);
+    const float x[4] = {lo.x, lo.y, hi.x, hi.y};
+    float p[4] = {x[1], x[0], x[3], x[2]};
+    if constexpr (MODE == kHalf || MODE == kAny) {
+        const float2 plo = act_f2<T>(r.p.x), phi = act_f2<T>(r.p.y);
+        p[0] = plo.x; p[1] = plo.y; p[2] = phi.x; p[3] = phi.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (MODE == kNone) {
+            y[i] = x[i];
+        } else {
             const int e = d + i;
-            if (e >= r) {
-                y[i] = x[i];
-                continue;
-            }
-            const bool first = a.pairs ? !(e & 1) : e < half;
-            const int u = a.pairs ? e / 2 : (first ? e : e - half);
-            const int partner = a.pairs ? (e ^ 1) : (first ? e + half : e - half);
-            const float xc = __fmul_rn(x[i], tab[u]), ps = __fmul_rn(act_f(row[partner]), tab[half + u]);
-            y[i] = first ? __fsub_rn(xc, ps) : __fadd_rn(xc, ps);
+            const bool first = MODE == kPairs || (MODE == kAny && a.pairs) ? !(i & 1) : e < a.rope_dim / 2;
+            const float xc = __fmul_rn(x[i], t.c[i]), ps = __fmul_rn(p[i], t.s[i]);
+            y[i] = e >= a.rope_dim ? x[i] : (first ? __fsub_rn(xc, ps) : __fadd_rn(xc, ps));
         }
     }
 }
 
-// The largest finite magnitude; NaN is stored as 0 (an infinity stays one, and saturates).
-__device__ __forceinline__ float absmax_finite(float (&y)[4], float m)
+// The largest finite magnitude; NaN is stored as 0.  An infinity stays one for the moment (`inf`):
+// it saturates once the scale is known.
+__device__ __forceinline__ float absmax_finite(float (&y)[4], float m, bool &inf)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (y[i] != y[i]) y[i] = 0.f;
         const float v = fabsf(y[i]);
+        inf |= v > FLT_MAX;
         m = v <= FLT_MAX ? fmaxf(m, v) : m;
     }
     return m;
 }
 
 template <bool F8>
-__device__ __forceinline__ uint32_t store_codes(float (&y)[4], float s, float r)
+__device__ __forceinline__ uint32_t store_codes(float (&y)[4], const CodeScale &cs, bool inf)
 {
-    // an infinity over a finite scale is the largest code
+    if (inf) {
+        const float most = (F8 ? 448.f : 127.f) * cs.s;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (fabsf(y[i]) > FLT_MAX) y[i] = copysignf(FLT_MAX, y[i]);
-    return codes4<F8>(y, s, r);
+        for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], -most), most);
+    }
+    return codes4<F8>(y, cs);
 }
 
-// Keys and values of one (sequence, page) item.  CH: chunks of 128 values of a head (a lane
-// has four of each).
-template <typename T, bool F8, int WPT, int CH>
-__device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, int head_block)
+// Keys or values of one head of a page, by WPT warps (wi: the warp among them).  CH: chunks of 128
+// values of a head (a lane has four of each).  s_max: one value per warp.
+template <typename T, bool F8, int WPT, int CH, Mode MODE>
+__device__ __forceinline__ void append_rows(const AppendArgs &a, const T *src, const float *tab, const KvPageSpan &ps,
+                                            int count, bool live, int head, int64_t page, float *scale, uint8_t *codes,
+                                            int wi, float *s_max)
+{
+    constexpr int kHeld = kHeldFloats / (4 * CH);
+    constexpr int kBatch = kHeld < 4 ? kHeld : 4;  // rows whose loads are in flight together
+    const int lane = threadIdx.x % 32, D = a.c.head_dim;
+    const int64_t row_stride = int64_t(a.q_heads + 2 * a.c.kv_heads) * D;
+    auto dim = [&](int c) { return 4 * (lane + 32 * c); };
+    auto at = [&](int c) { return min(dim(c), D - 4); };
+    auto turned = [&](int r, int c, float (&y)[4]) {
+        turn4<T, MODE>(a, at(c), load_raw<T, MODE>(a, src + r * row_stride, at(c)),
+                       load_turn<MODE>(a, tab + int64_t(r) * a.rope_dim, at(c)), y);
+    };
+    float held[kHeld][CH][4];
+    float amax = 0.f, before = 0.f;
+    bool inf = false;
+    if (live && wi < count) {
+        if (ps.off > 0) before = *scale;
+#pragma unroll
+        for (int i0 = 0; i0 < kHeld; i0 += kBatch) {
+            if (wi + i0 * WPT >= count) break;
+            Raw raw[kBatch][CH];
+            Turn turn[kBatch][CH];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = min(wi + (i0 + i) * WPT, count - 1);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    raw[i][c] = load_raw<T, MODE>(a, src + r * row_stride, at(c));
+                    turn[i][c] = load_turn<MODE>(a, tab + int64_t(r) * a.rope_dim, at(c));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    // a row or lane of the repeated address repeats its values: the maximum is the same
+                    turn4<T, MODE>(a, at(c), raw[i][c], turn[i][c], held[i0 + i][c]);
+                    amax = absmax_finite(held[i0 + i][c], amax, inf);
+                }
+        }
+        for (int r = wi + kHeld * WPT; r < count; r += WPT)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                float y[4];
+                turned(r, c, y);
+                amax = absmax_finite(y, amax, inf);
+            }
+        amax = __uint_as_float(warp_umax(__float_as_uint(amax)));
+    }
+    if constexpr (WPT > 1) {
+        if (lane == 0) s_max[wi] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WPT; ++i) amax = fmaxf(amax, s_max[i]);
+        if (live && wi >= count && ps.off > 0) before = *scale;
+        __syncthreads();  // every warp has read the scale before it is replaced
+    } else {
+        __syncwarp();
+    }
+    if (!live) return;
+    const float now = fmaxf(before, __fmul_rn(amax, kInvQmax<F8>));
+    if (wi == 0 && lane == 0) *scale = now;
+    if (now > before && ps.off > 0) {  // the page's earlier tokens in the new scale
+        const float ratio = __fdiv_rn(before, now);
+        const CodeScale one = code_scale(1.f);
+        for (int r = wi; r < ps.off; r += WPT)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (dim(c) >= D) continue;
+                uint32_t *p = reinterpret_cast<uint32_t *>(codes + int64_t(r) * a.pitch + dim(c));
+                const uint32_t w = *p;
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(code_value<F8>(w, i), ratio);
+                *p = codes4<F8>(y, one);
+            }
+    }
+    const CodeScale cs = code_scale(now);
+    codes += int64_t(ps.off) * a.pitch;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int r = wi + i * WPT;
+        if (r >= count) break;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t w = store_codes<F8>(held[i][c], cs, inf);
+            if (dim(c) < D) *reinterpret_cast<uint32_t *>(codes + int64_t(r) * a.pitch + dim(c)) = w;
+        }
+    }
+    for (int r = wi + kHeld * WPT; r < count; r += WPT)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float y[4];
+            turned(r, c, y);
+            absmax_finite(y, 0.f, inf);
+            const uint32_t w = store_codes<F8>(y, cs, inf);
+            if (dim(c) < D) *reinterpret_cast<uint32_t *>(codes + int64_t(r) * a.pitch + dim(c)) = w;
+        }
+}
+
+// Keys and values of one (sequence, page) item.
+template <typename T, bool F8, int WPT, int CH, Mode MODE>
+__device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, int part)
 {
     constexpr int kTasks = kWarps / WPT;  // (head, keys or values) pairs of the block
-    constexpr int kHeld = kHeldFloats / (4 * CH);
     __shared__ int s_seq[4];
     __shared__ float s_max[kWarps];
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = tid / 32;
     if (tid == 0) s_seq[0] = -1;
     __syncthreads();
     for (int b = tid; b < a.n_seqs; b += kThreads) {
@@ -158,106 +306,33 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, i
     const int b = s_seq[0];
     if (b < 0) return;
     const KvSpan span = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
-    KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift), a.page_shift);
+    const KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift), a.page_shift);
     if (ps.count == 0) return;
     const int pos0 = (ps.page << a.page_shift) + ps.off;
     const int count = min(ps.count, a.limit - pos0);  // positions beyond the rope table have no place
-    const int64_t page = kv_page_ok(a.block_table[int64_t(b) * a.max_pages + ps.page], a.c.num_pages);
+    const int64_t page = kv_page_ok(__ldg(a.block_table + int64_t(b) * a.max_pages + ps.page), a.c.num_pages);
     if (tid == 0 && (page < 0 || count < ps.count || s_seq[3] > a.capacity))
         atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
     if (page < 0 || count <= 0) return;
 
     const int task = warp / WPT, wi = warp % WPT;
-    const int pair = head_block * kTasks + task;  // keys of head h, then its values
-    const int head = pair / 2;
-    const bool is_k = (pair & 1) == 0, live = head < a.c.kv_heads;
-    const int D = a.c.head_dim;
-    const int64_t row_stride = int64_t(a.q_heads + 2 * a.c.kv_heads) * D;
-    const T *src = static_cast<const T *>(a.qkv) + int64_t(ps.token) * row_stride +
+    const int pair = part * kTasks + task;  // keys of head h, then its values
+    const int head = min(pair / 2, a.c.kv_heads - 1), D = a.c.head_dim;
+    const bool is_k = (pair & 1) == 0, live = pair < 2 * a.c.kv_heads;
+    const T *src = static_cast<const T *>(a.qkv) + int64_t(ps.token) * (a.q_heads + 2 * a.c.kv_heads) * D +
                    int64_t(a.q_heads + (is_k ? 0 : a.c.kv_heads) + head) * D;
-    const float *tab = is_k && a.rope_dim ? a.rope + int64_t(pos0) * a.rope_dim : nullptr;
-    float held[kHeld][CH][4];
-    float amax = 0.f, before = 0.f;
-    const int64_t si = kv_scale_index(page, head, a.c.kv_heads);
-    float *scale = (is_k ? a.c.k_scale : a.c.v_scale) + si;
-    if (live) {
-        if (ps.off > 0) before = *scale;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int r = wi + i * WPT;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int d = 4 * (lane + 32 * c);
-                if (r < count && d < D) {
-                    load_turned<T>(a, src + r * row_stride, d, tab ? tab + int64_t(r) * a.rope_dim : nullptr, held[i][c]);
-                    amax = absmax_finite(held[i][c], amax);
-                }
-            }
-        }
-        for (int r = wi + kHeld * WPT; r < count; r += WPT)
-            for (int c = 0; c < CH; ++c) {
-                const int d = 4 * (lane + 32 * c);
-                if (d >= D) continue;
-                float y[4];
-                load_turned<T>(a, src + r * row_stride, d, tab ? tab + int64_t(r) * a.rope_dim : nullptr, y);
-                amax = absmax_finite(y, amax);
-            }
-        amax = __uint_as_float(warp_umax(__float_as_uint(amax)));
-    }
-    if (WPT > 1) {
-        if (lane == 0) s_max[warp] = amax;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < WPT; ++i) amax = fmaxf(amax, s_max[task * WPT + i]);
-    } else {
-        __syncwarp();
-    }
-    if (!live) return;
-    const float need = __fmul_rn(amax, kInvQmax<F8>);
-    const float now = fmaxf(before, need);
-    const float rnow = now != 0.f ? __frcp_rn(now) : 0.f;
-    if (wi == 0 && lane == 0) *scale = now;
+    float *scale = (is_k ? a.c.k_scale : a.c.v_scale) + kv_scale_index(page, head, a.c.kv_heads);
     uint8_t *codes = static_cast<uint8_t *>(is_k ? a.c.k : a.c.v) +
                      kv_code_offset(page, head, 0, a.c.kv_heads, a.page_shift, a.pitch);
-    if (now > before && ps.off > 0) {  // the page's earlier tokens in the new scale
-        const float ratio = __fdiv_rn(before, now);
-        for (int r = wi; r < ps.off; r += WPT)
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int d = 4 * (lane + 32 * c);
-                if (d >= D) continue;
-                uint32_t *p = reinterpret_cast<uint32_t *>(codes + int64_t(r) * a.pitch + d);
-                const uint32_t w = *p;
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(code_value<F8>(w, i), ratio);
-                *p = codes4<F8>(y, 1.f, 1.f);
-            }
-    }
-    codes += int64_t(ps.off) * a.pitch;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int r = wi + i * WPT;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int d = 4 * (lane + 32 * c);
-            if (r < count && d < D)
-                *reinterpret_cast<uint32_t *>(codes + int64_t(r) * a.pitch + d) = store_codes<F8>(held[i][c], now, rnow);
-        }
-    }
-    for (int r = wi + kHeld * WPT; r < count; r += WPT)
-        for (int c = 0; c < CH; ++c) {
-            const int d = 4 * (lane + 32 * c);
-            if (d >= D) continue;
-            float y[4];
-            load_turned<T>(a, src + r * row_stride, d, tab ? tab + int64_t(r) * a.rope_dim : nullptr, y);
-            absmax_finite(y, 0.f);
-            *reinterpret_cast<uint32_t *>(codes + int64_t(r) * a.pitch + d) = store_codes<F8>(y, now, rnow);
-        }
+    if (MODE != kNone && is_k)  // (one answer for the warps of a task, and with WPT > 1 for the block)
+        append_rows<T, F8, WPT, CH, MODE>(a, src, a.rope + int64_t(pos0) * a.rope_dim, ps, count, live, head, page, scale,
+                                          codes, wi, s_max);
+    else
+        append_rows<T, F8, WPT, CH, kNone>(a, src, nullptr, ps, count, live, head, page, scale, codes, wi, s_max);
 }
 
 // The queries of q_tokens tokens: kWarps / q_tokens warps take a token's heads in turn.
-template <typename T, int CH>
+template <typename T, int CH, Mode MODE>
 __device__ __forceinline__ void turn_queries(const AppendArgs &a, int64_t block)
 {
     __shared__ int s_pos[kWarps];  // position; -1: no place; -2: not part of a sequence
@@ -282,38 +357,65 @@ __device__ __forceinline__ void turn_queries(const AppendArgs &a, int64_t block)
     const int D = a.c.head_dim;
     const T *src = static_cast<const T *>(a.qkv) + m * int64_t(a.q_heads + 2 * a.c.kv_heads) * D;
     T *dst = static_cast<T *>(a.q_out) + m * int64_t(a.q_heads) * D;
-    const float *tab = a.rope_dim && pos >= 0 ? a.rope + int64_t(pos) * a.rope_dim : nullptr;
-    for (int h = warp % per; h < a.q_heads; h += per)
+    const float *tab = MODE == kNone ? nullptr : a.rope + int64_t(max(pos, 0)) * a.rope_dim;
+    constexpr int kBatch = 8 / CH;  // heads whose loads are in flight together
+    Turn turn[CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int d = 4 * (lane + 32 * c);
-            if (d >= D) continue;
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            if (pos >= 0) load_turned<T>(a, src + int64_t(h) * D, d, tab, y);
-            *reinterpret_cast<uint2 *>(dst + int64_t(h) * D + d) = make_uint2(act_t2<T>(y[0], y[1]), act_t2<T>(y[2], y[3]));
-        }
+    for (int c = 0; c < CH; ++c) turn[c] = load_turn<MODE>(a, tab, min(4 * (lane + 32 * c), D - 4));
+    for (int h0 = warp % per; h0 < a.q_heads; h0 += per * kBatch) {
+        Raw raw[kBatch][CH];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                raw[i][c] = load_raw<T, MODE>(a, src + int64_t(min(h0 + i * per, a.q_heads - 1)) * D,
+                                              min(4 * (lane + 32 * c), D - 4));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int h = h0 + i * per, d = 4 * (lane + 32 * c);
+                if (h >= a.q_heads || d >= D) continue;
+                float y[4];
+                turn4<T, MODE>(a, d, raw[i][c], turn[c], y);
+                if (pos < 0) y[0] = y[1] = y[2] = y[3] = 0.f;
+                *reinterpret_cast<uint2 *>(dst + int64_t(h) * D + d) =
+                    make_uint2(act_t2<T>(y[0], y[1]), act_t2<T>(y[2], y[3]));
+            }
+    }
 }
 
-template <typename T, bool F8, int WPT, int CH>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a)
+template <typename T, bool F8, int WPT, int CH, Mode MODE>
+__global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : 2) kv_append_kernel(const __grid_constant__ AppendArgs a)
 {
     grid_dep_launch();
     grid_dep_wait();  // the QKV projection and the batch's arrays may come from the kernel before
-    const int64_t kv_blocks = a.kv_items * a.head_blocks;
+    const int64_t kv_blocks = a.kv_items * a.parts;
     if (int64_t(blockIdx.x) < kv_blocks)
-        append_item<T, F8, WPT, CH>(a, blockIdx.x / a.head_blocks, blockIdx.x % a.head_blocks);
+        append_item<T, F8, WPT, CH, MODE>(a, blockIdx.x / a.parts, blockIdx.x % a.parts);
     else
-        turn_queries<T, CH>(a, blockIdx.x - kv_blocks);
+        turn_queries<T, CH, MODE>(a, blockIdx.x - kv_blocks);
 }
 
-template <typename T, bool F8>
+template <typename T, bool F8, Mode MODE>
 const void *append_kernel(bool many, bool wide)
 {
     if (many)
-        return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, 4, 2>)
-                    : reinterpret_cast<const void *>(kv_append_kernel<T, F8, 4, 1>);
-    return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, 2>)
-                : reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, 1>);
+        return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, kWarps, 2, MODE>)
+                    : reinterpret_cast<const void *>(kv_append_kernel<T, F8, kWarps, 1, MODE>);
+    return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, 2, MODE>)
+                : reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, 1, MODE>);
+}
+
+template <typename T, bool F8>
+const void *append_kernel(Mode mode, bool many, bool wide)
+{
+    switch (mode) {
+    case kNone: return append_kernel<T, F8, kNone>(many, wide);
+    case kPairs: return append_kernel<T, F8, kPairs>(many, wide);
+    case kHalf: return append_kernel<T, F8, kHalf>(many, wide);
+    default: return append_kernel<T, F8, kAny>(many, wide);
+    }
 }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -385,21 +487,22 @@ extern "C" wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t 
     a.capacity = int(batch->max_pages * cache->page_size);
     a.limit = rope ? int(std::min<int64_t>(a.capacity, rope_len)) : a.capacity;
     a.pairs = rope_style == WQ_ROPE_PAIRS;
-    // WQ_ROPE_HALF: a value's partner is rope_dim / 2 away, and its four cos / sin lie at that
-    // multiple too; a table row is rope_dim values long
-    a.vec = a.pairs ? rope_dim % 4 == 0 : rope_dim % 8 == 0;
+    // kHalf: partners and cos / sin at rope_dim / 2, a table row rope_dim values long; see Mode
+    const Mode mode = !rope_dim                           ? kNone
+                      : a.pairs                           ? (rope_dim % 4 == 0 ? kPairs : kAny)
+                      : rope_dim % 8 == 0 ? kHalf : kAny;
     a.kv_items = (M >> a.page_shift) + 2 * batch->n_seqs;
-    // A page's rows go over four warps where sequences bring many tokens, else one warp takes
-    // each (head, keys or values).
+    // A page's rows go over all warps of a block where sequences bring many tokens, else one warp
+    // takes each (head, keys or values).
     const bool many = M >= 4 * batch->n_seqs;
-    a.head_blocks = many ? cache->kv_heads : (cache->kv_heads + 3) / 4;
+    a.parts = many ? 2 * cache->kv_heads : (2 * cache->kv_heads + kWarps - 1) / kWarps;
     a.q_tokens = M <= 1024 ? 1 : kWarps;
-    const int64_t blocks = a.kv_items * a.head_blocks + (M + a.q_tokens - 1) / a.q_tokens;
+    const int64_t blocks = a.kv_items * a.parts + (M + a.q_tokens - 1) / a.q_tokens;
     if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
     const bool wide = cache->head_dim > 128, f8 = cache->format == WQ_FMT_E4M3;
-    const void *fn = dt == WQ_F16 ? (f8 ? append_kernel<__half, true>(many, wide) : append_kernel<__half, false>(many, wide))
-                                  : (f8 ? append_kernel<__nv_bfloat16, true>(many, wide)
-                                        : append_kernel<__nv_bfloat16, false>(many, wide));
+    const void *fn = dt == WQ_F16 ? (f8 ? append_kernel<__half, true>(mode, many, wide) : append_kernel<__half, false>(mode, many, wide))
+                                  : (f8 ? append_kernel<__nv_bfloat16, true>(mode, many, wide)
+                                        : append_kernel<__nv_bfloat16, false>(mode, many, wide));
     PreparedLaunch L;
     L.set(fn, dim3(unsigned(blocks)), dim3(kThreads), 0, a);
     return launch_prepared(L, stream, "kv_append_kernel");

@@ -82,10 +82,10 @@ __device__ __forceinline__ uint32_t absmax8(const float (&y)[8], uint32_t m)
 }
 
 template <bool F8>
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float s, float r)
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], const CodeScale &c)
 {
     const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
-    return make_uint2(codes4<F8>(lo, s, r), codes4<F8>(hi, s, r));
+    return make_uint2(codes4<F8>(lo, c), codes4<F8>(hi, c));
 }
 
 // V: vectors a thread holds (0: the row is too long to hold; h is read back for the two
@@ -177,8 +177,7 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(const __gri
     // a row that holds an infinity or NaN: scale NaN (its products are NaN), codes 0
     const bool finite = amax < 0x7f800000u;
     const float sc = finite ? __fmul_rn(__uint_as_float(amax), kInvQmax<F8>) : __uint_as_float(0x7fc00000u);
-    const float s = finite ? sc : 0.f;
-    const float rc = s != 0.f ? __frcp_rn(s) : 0.f;
+    const CodeScale cs = code_scale(finite ? sc : 0.f);
     if (tid == 0) a.a_scale[row] = sc;
     if constexpr (V > 0) {
 #pragma unroll
@@ -186,13 +185,13 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(const __gri
             const int64_t j = tid + int64_t(i) * nt;
             float y[8];
             scaled8<T>(hv[i], gv[i], rstd, y);
-            if (j < a.K8) q[j] = codes8<F8>(y, s, rc);
+            if (j < a.K8) q[j] = finite ? codes8<F8>(y, cs) : make_uint2(0, 0);
         }
     } else {
         for (int64_t j = tid; j < a.K8; j += nt) {
             float y[8];
             scaled8<T>(back[j], __ldg(gamma + j), rstd, y);
-            q[j] = codes8<F8>(y, s, rc);
+            q[j] = finite ? codes8<F8>(y, cs) : make_uint2(0, 0);
         }
     }
 }
