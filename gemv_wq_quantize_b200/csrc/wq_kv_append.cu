@@ -429,12 +429,13 @@ wq_status check_kv(const wq_kv_cache *c, const wq_kv_batch *b, wq_dtype dt, int6
     if (M <= 0) return fail(WQ_ERR_INVALID_ARG, "M must be positive");
     if (c->format != WQ_FMT_INT && c->format != WQ_FMT_E4M3)
         return fail(WQ_ERR_INVALID_ARG, "cache format must be WQ_FMT_INT (INT8) or WQ_FMT_E4M3");
-    if (c->num_pages <= 0 || c->num_pages > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "num_pages must be 1 .. 2^31 - 1");
+    if (c->num_pages <= 0) return fail(WQ_ERR_INVALID_ARG, "num_pages must be positive");
     if (c->page_size < kKvMinPage || c->page_size > kKvMaxPage || (c->page_size & (c->page_size - 1)))
         return fail(WQ_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
     if (c->head_dim < 16 || c->head_dim > kKvMaxHeadDim || c->head_dim % 4)
         return fail(WQ_ERR_UNSUPPORTED, "head_dim must be a multiple of 4 from 16 to 256");
     if (c->kv_heads < 1 || c->kv_heads > 1024) return fail(WQ_ERR_INVALID_ARG, "kv_heads must be 1 .. 1024");
+    if (c->num_pages > 0x7fffffff / int64_t(c->kv_heads)) return fail(WQ_ERR_INVALID_ARG, "num_pages * kv_heads exceeds int32");
     if (q_heads < 1 || q_heads % c->kv_heads) return fail(WQ_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
     if (M > 0x7fffffff / int64_t(q_heads)) return fail(WQ_ERR_INVALID_ARG, "M * q_heads exceeds int32");
     if (b->n_seqs < 1) return fail(WQ_ERR_INVALID_ARG, "n_seqs must be positive");

@@ -1,23 +1,28 @@
-// wq_kv_attn.cu -- kv_attention for few rows per key head (decode and draft verification):
-// attention over the paged 8-bit cache, split over the whole GPU by key ranges.
+// wq_kv_attn.cu -- kv_attention: the C entry points, and the kernel for few rows per key head
+// (decode and draft verification): attention over the paged 8-bit cache, split over the whole
+// GPU by key ranges.
 //
 // Mathematics: for a query row q of position p and the keys j <= p of its sequence,
 //   s_j = sm_scale * ks[page(j)] * (q . kc_j),   out = sum_j softmax(s)_j vs[page(j)] vc_j
 // with the codes kc, vc exact in binary16, products on mma.sync with binary32 accumulation, one
 // pass with a running maximum and sum, and the two page scales applied in binary32.
 //
-// Bound by reading the cache once: a group of query heads shares a key head's codes, so the
-// rows of (sequence, key head) form the 8-wide N side of both products (S^T = K Q^T and
-// O^T = V^T P^T): the codes are the 16-row A operand, nothing is wasted on padding up to 8 rows,
-// and codes go from global memory straight into the registers of the lane that multiplies them
-// (a dot product may take its dimensions in any order, so a lane's 16 contiguous bytes of a key
-// are its fragments of four steps; a lane's 16 contiguous bytes of four values are its fragments
-// of eight row tiles).  No shared memory on the way, so many loads stay in flight.
+// Bound by reading the cache once.  A group of query heads shares a key head's codes, so the rows
+// of (sequence, key head) form the 8-wide N side of both products (S^T = K Q^T and
+// O^T = V^T P^T): the codes are the 16-row A operand and nothing is wasted on padding up to 8
+// rows (an M side of 128 rows of tcgen05 would be 8 of 128 full).  Every warp walks its own keys
+// with a small ring of its own: TMA copies of 32 keys or values (16 at head sizes above 128) into
+// swizzled shared memory, the next ones issued by the warp as soon as it has read a buffer, so
+// two are in flight while it multiplies a third and no warp waits for another between the ends of
+// a tile.  The swizzle makes the fragment reads free of bank conflicts; a dot product may take its
+// dimensions in any order, so a lane's 16 contiguous bytes of a key are its fragments of four MMA
+// steps, and its 16 contiguous bytes of four values are its fragments of eight row tiles.
 //
-// Work split: tiles (sequence, key head, 8 * NT rows) are cut into units of kUnit keys, and the
-// persistent blocks take equal contiguous shares of all units, whatever the lengths.  A tile cut
-// over several blocks leaves partial sums in the workspace; the last block to arrive adds them
-// in the order of their keys, so the result does not depend on which block that is.
+// Work split: tiles (sequence, key head, 8 * NT rows) are cut into units of 64 keys, and the
+// persistent blocks take equal contiguous shares of all units, whatever the lengths (a tile counts
+// kTileUnits more, about what its start and end take).  A tile cut over several blocks leaves
+// partial sums in the workspace; the last block to arrive adds them in the order of their keys,
+// so the result does not depend on which block that is.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,7 +35,7 @@
 
 namespace wq {
 
-__device__ int g_kv_attn_error;
+static __device__ int g_kv_attn_error;
 
 int kv_attn_read_error()
 {
@@ -42,9 +47,12 @@ int kv_attn_read_error()
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 6;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 64;  // keys of a unit: the granule of the split
+constexpr int kUnitShift = 6;     // a unit: 64 keys, the granule of the split
+constexpr int kTileUnits = 6;     // what the start and end of a tile cost a block, in units
+constexpr int kLeastUnits = 4;    // of a share: a stage for each warp; less only adds partials
+constexpr int kMostUnits = 1 << 30;
 
 // exp2 arguments are raised by 15: the weights then reach 2^15 in binary16 (its largest is just
 // below 2^16) and keep full precision down to 2^-29 of the largest weight, so that many small
@@ -58,90 +66,100 @@ __device__ __forceinline__ uint32_t trans8x8(uint32_t x)
     return d;
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
+__device__ __forceinline__ uint64_t globaltimer()
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p)
-{
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
 }
 
 // DT: head_dim rounded up to 64, 128 or 256.  NT: tiles of 8 rows.
 template <int DT, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kSteps = DT >= 256 || NT > 1 ? 1 : 2;  // 16-key steps of an iteration
-    static constexpr int kRowFloats = DT + 2;    // a partial row: sums, maximum, weight sum
+    static constexpr int kPerSm = DT <= 128 && NT == 1 ? 2 : 1;  // blocks: 128 or 255 registers a thread
+    static constexpr int kSteps = DT <= 128 ? 2 : 1;             // 16-key steps of a stage
+    static constexpr int kKeys = 16 * kSteps;
+    static constexpr int kRowBytes = DT < 128 ? 64 : 128;        // of a copied box; two boxes at DT 256
+    static constexpr int kBoxes = DT / 128 < 1 ? 1 : DT / 128;
+    static constexpr int kBoxBytes = kKeys * kRowBytes;
+    static constexpr int kItem = kBoxBytes * kBoxes;             // the keys (or values) of a stage
+    static constexpr int kBufs = kPerSm == 2 ? 4 : 5;            // items of a warp's ring
+    static constexpr int kRowFloats = DT + 4;                    // a partial row: sums, maximum, weight sum
 };
 
 // A row of sums in shared memory and in the workspace is kept in the order of the fragments:
-// place 16 i + 2 g + e holds dimension DT / 8 * g + 2 i + e (lane (g, j) then stores pairs
-// without bank conflicts, rows being DT + 4 apart).
+// place 16 i + 2 g + e holds dimension dim_of(that) (lane (g, j) then stores pairs without bank
+// conflicts, rows being DT + 4 apart).
 template <int DT>
 __device__ __forceinline__ int dim_of(int place)
 {
-    return DT / 8 * (place % 16 / 2) + 2 * (place / 16) + place % 2;
+    const int i = place / 16, g = place % 16 / 2, e = place % 2;
+    return DT == 64 ? 8 * g + 2 * i + e : 128 * (i / 8) + 16 * g + 2 * (i % 8) + e;
 }
 
 template <int DT, int NT>
 struct Smem {
-    float o[kWarps][8 * NT][DT + 4];
-    float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    int64_t sums[kWarps + 1];
-    unsigned last;
+    using S = Shape<DT, NT>;
+    alignas(1024) uint8_t ring[kWarps][S::kBufs][S::kItem];
+    uint64_t full[kWarps][S::kBufs];
+    float o[kWarps][8 * NT][DT / 4 + 4];   // a quarter of the warps' sums at a time
+    float m[kWarps][8 * NT], l[kWarps][8 * NT], f[kWarps][8 * NT];
+    float top[8 * NT], weight[8 * NT];     // of a row over the warps
+    int64_t sums[kWarps];
+    int first[2], parts[2];                // the tiles that this block left partials of
+    int abort;
     // then the unit counts of all sequences up to each (n_seqs + 1)
 };
 
-// The codes of 16 keys in the registers of a warp.
-template <int DT>
-struct KeyRegs {
-    uint4 r[2][DT / 64];  // lane (g, j): keys g and g + 8, bytes 64 c + 16 j
-};
-template <int DT>
-struct ValRegs {
-    uint32_t w[4][DT / 32];  // lane (g, j): keys 2j, 2j + 1, 2j + 8, 2j + 9, bytes DT / 8 * g
-};
-
-template <int DT>
-__device__ __forceinline__ void load_keys(KeyRegs<DT> &k, const uint8_t *base, int pitch, int g, int j)
+// A bounded wait with one answer for the warp: about 2 s, or 20 ms once another warp gave up.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int c = 0; c < DT / 64; ++c) {
-            const int d = 64 * c + 16 * j;
-            k.r[t][c] = d < pitch ? ldg_stream(base + (g + 8 * t) * pitch + d) : make_uint4(0, 0, 0, 0);
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait_short(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer();
+        while (!ok) {
+            for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait_short(bar, parity);
+            if (!ok && globaltimer() - t0 > (*abort ? 20000000ull : 2000000000ull)) {
+                atomicCAS(&g_kv_attn_error, kErrNone, kErrWaitTimeout);
+                *abort = 1;
+                break;
+            }
         }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
+// The codes of 16 keys of a stage in the registers of a warp, from swizzled shared memory.
+// Keys: lane (g, j) has keys g and g + 8, dimensions kdim(c, j) .. + 15.
 template <int DT>
-__device__ __forceinline__ void load_vals(ValRegs<DT> &v, const uint8_t *base, int pitch, int g, int j)
+__device__ __forceinline__ int kdim(int c, int j)
 {
+    return DT == 64 ? 16 * j : 128 * (c / 2) + 32 * j + 16 * (c % 2);
+}
+template <int DT, int NT>
+__device__ __forceinline__ uint4 key_chunk(const uint8_t *k, int row, int c, int j)
+{
+    if constexpr (DT == 64) return lds128(k + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
+    else return lds128(k + c / 2 * Shape<DT, NT>::kBoxBytes + row * 128 + (((2 * j + c % 2) ^ (row & 7)) << 4));
+}
+// Values: lane (g, j) has keys 2j, 2j + 1, 2j + 8, 2j + 9 and DT / 8 bytes of each.
+template <int DT, int NT>
+__device__ __forceinline__ void value_words(const uint8_t *v, int row, int g, uint32_t (&w)[DT / 32])
+{
+    if constexpr (DT == 64) {
+        const uint2 x = lds64(v + row * 64 + (((g / 2) ^ ((row >> 1) & 3)) << 4) + 8 * (g % 2));
+        w[0] = x.x;
+        w[1] = x.y;
+    } else {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const uint8_t *p = base + (2 * j + (t & 1) + 8 * (t >> 1)) * pitch;
-        if constexpr (DT == 64) {
-            const int d = 8 * g;
-            const uint2 x = d < pitch ? ldg_stream8(p + d) : make_uint2(0, 0);
-            v.w[t][0] = x.x;
-            v.w[t][1] = x.y;
-        } else {
-#pragma unroll
-            for (int c = 0; c < DT / 128; ++c) {
-                const int d = DT / 8 * g + 16 * c;
-                const uint4 x = d < pitch ? ldg_stream(p + d) : make_uint4(0, 0, 0, 0);
-                v.w[t][4 * c] = x.x;
-                v.w[t][4 * c + 1] = x.y;
-                v.w[t][4 * c + 2] = x.z;
-                v.w[t][4 * c + 3] = x.w;
-            }
+        for (int c = 0; c < DT / 128; ++c) {
+            const uint4 x = lds128(v + c * Shape<DT, NT>::kBoxBytes + row * 128 + ((g ^ (row & 7)) << 4));
+            w[4 * c] = x.x;
+            w[4 * c + 1] = x.y;
+            w[4 * c + 2] = x.z;
+            w[4 * c + 3] = x.w;
         }
     }
 }
@@ -149,12 +167,12 @@ __device__ __forceinline__ void load_vals(ValRegs<DT> &v, const uint8_t *base, i
 // One warp's running state over its keys: column n of the products is row n of the tile.
 template <int DT, int NT>
 struct State {
-    float o[NT][DT / 16][4];  // lane (g, j): dimensions of tile i: DT/8 g + 2i and + 1; rows 2j, 2j + 1
+    float o[NT][DT / 16][4];  // lane (g, j): places 16 i + 2 g and + 1; rows 2j, 2j + 1
     float m[NT][2], l[NT][2];
 };
 
-// Queries as B fragments (binary16): k-step c * 4 + w holds, for lane (g, j) and row g, the
-// dimensions 64 c + 16 j + 4 w .. + 3.  A bfloat16 row is scaled by a power of two so that its
+// Queries as B fragments (binary16): k-step 4 c + w holds, for lane (g, j) and row g, the
+// dimensions kdim(c, j) + 4 w .. + 3.  A bfloat16 row is scaled by a power of two so that its
 // largest value fits binary16; what falls below the smallest subnormal there is under 2^-25 of
 // the row's largest value, the size of the binary32 accumulation's own rounding.  The scale's
 // inverse comes back for rows 2j and 2j + 1.
@@ -174,7 +192,7 @@ __device__ __forceinline__ void load_queries(const KvAttnArgs &a, const KvSpan &
         for (int c = 0; c < DT / 64; ++c)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const int d = 64 * c + 16 * j + 4 * w;
+                const int d = kdim<DT>(c, j) + 4 * w;
                 const uint2 x = live && d < a.head_dim ? *reinterpret_cast<const uint2 *>(q + d) : make_uint2(0, 0);
                 qf[n][4 * c + w][0] = x.x;
                 qf[n][4 * c + w][1] = x.y;
@@ -203,9 +221,10 @@ __device__ __forceinline__ void load_queries(const KvAttnArgs &a, const KvSpan &
     }
 }
 
-// Scores of 16 keys: S^T[key][row], lane (g, j) holds keys g and g + 8, rows 2j and 2j + 1.
+// Scores of 16 keys (rows row0 .. + 15 of a stage): S^T[key][row], lane (g, j) holds keys g and
+// g + 8, rows 2j and 2j + 1.
 template <bool F8, int DT, int NT>
-__device__ __forceinline__ void scores(const KeyRegs<DT> &k, const uint32_t (&qf)[NT][DT / 16][2], float (&s)[NT][4])
+__device__ __forceinline__ void scores(const uint8_t *k, int row0, int g, int j, const uint32_t (&qf)[NT][DT / 16][2], float (&s)[NT][4])
 {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -213,7 +232,8 @@ __device__ __forceinline__ void scores(const KeyRegs<DT> &k, const uint32_t (&qf
         for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
 #pragma unroll
     for (int c = 0; c < DT / 64; ++c) {
-        const uint32_t *lo = &k.r[0][c].x, *hi = &k.r[1][c].x;
+        const uint4 r0 = key_chunk<DT, NT>(k, row0 + g, c, j), r1 = key_chunk<DT, NT>(k, row0 + g + 8, c, j);
+        const uint32_t lo[4] = {r0.x, r0.y, r0.z, r0.w}, hi[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const uint32_t x = F8 ? lo[w] : lo[w] ^ 0x80808080u, y = F8 ? hi[w] : hi[w] ^ 0x80808080u;
@@ -224,17 +244,28 @@ __device__ __forceinline__ void scores(const KeyRegs<DT> &k, const uint32_t (&qf
     }
 }
 
-// O^T += vs * (V^T P^T) over 16 keys; p: the weights as B fragments.
+// O^T += vs * (V^T P^T) over 16 keys; p: the weights as B fragments.  left: keys of the 16 that
+// hold codes (the slots behind may hold e4m3 NaN codes).
 template <bool F8, int DT, int NT>
-__device__ __forceinline__ void add_values(const ValRegs<DT> &v, const uint32_t (&p)[NT][2], float vs, State<DT, NT> &st)
+__device__ __forceinline__ void add_values(const uint8_t *v, int row0, int left, int g, int j,
+                                           const uint32_t (&p)[NT][2], float vs, State<DT, NT> &st)
 {
+    uint32_t w[4][DT / 32];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int key = 2 * j + (t & 1) + 8 * (t >> 1);
+        value_words<DT, NT>(v, row0 + key, g, w[t]);
+        if (F8 && left < 16 && key >= left)
+#pragma unroll
+            for (int x = 0; x < DT / 32; ++x) w[t][x] = 0u;
+    }
 #pragma unroll
     for (int i = 0; i < DT / 16; i += 2) {
         // bytes 2i .. 2i + 3 of the lane's chunk of four keys: row tiles i and i + 1
-        const uint32_t x0 = v.w[0][i / 2], x1 = v.w[1][i / 2], x2 = v.w[2][i / 2], x3 = v.w[3][i / 2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            uint32_t a = prmt(x0, x1, e ? 0x7362 : 0x5140), b = prmt(x2, x3, e ? 0x7362 : 0x5140);
+            uint32_t a = prmt(w[0][i / 2], w[1][i / 2], e ? 0x7362 : 0x5140);
+            uint32_t b = prmt(w[2][i / 2], w[3][i / 2], e ? 0x7362 : 0x5140);
             if constexpr (!F8) {
                 a ^= 0x80808080u;
                 b ^= 0x80808080u;
@@ -254,397 +285,581 @@ __device__ __forceinline__ void add_values(const ValRegs<DT> &v, const uint32_t 
 struct Tile {
     KvSpan s;
     int b, head, row0, rows;
-    int keys;  // keys that the tile's last row sees
+    int keys;      // keys that the tile's last row sees
+    int t0, t1;    // keys of this block's units of the tile
+    int u0, u1;    // units of the tile, counted over all sequences: the first that holds keys, the end
+    bool first;    // this block's part begins the tile's keys, and
+    bool whole;    // ends them
 };
 
-// The running state over keys [t0, t1) of the tile, 16-key steps taken in turn by the warps.
-template <bool F8, bool BF16, int DT, int NT>
-__device__ __forceinline__ void walk_keys(const KvAttnArgs &a, const Tile &t, int t0, int t1, State<DT, NT> &st)
+// The tile of unit u and this block's part of it (units up to u_end); next: the unit behind it.
+// A part without keys (of a tile's first kTileUnits units alone) has t1 = t0 and is passed over,
+// but for the first part of a tile that has none at all.
+template <int ROWS>
+__device__ __forceinline__ Tile tile_of(const KvAttnArgs &a, const int *before, int shift, int u, int u_end, int &next)
 {
+    // the sequence of unit u: the last b with before[b] <= u (empty ones have no units)
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (before[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    Tile t;
+    t.b = lo;
+    t.s = kv_span(__ldg(a.cu_q + lo), __ldg(a.cu_q + lo + 1), __ldg(a.seq_len + lo), a.M, a.capacity);
+    const bool split = a.partials != nullptr;
+    const int head_units = split ? kTileUnits : 0;
+    const int units = split ? head_units + int(kv_units(t.s.len, 1 << shift)) : 1;
+    const int tiles = (t.s.n * a.group + ROWS - 1) / ROWS;
+    const int item = (u - before[lo]) / units;  // (key head, tile) of the sequence
+    const int begin = before[lo] + item * units, end = begin + units;
+    next = min(end, u_end);
+    t.head = item / tiles;
+    t.row0 = item % tiles * ROWS;
+    t.rows = min(ROWS, t.s.n * a.group - t.row0);
+    t.keys = max(0, t.s.len - t.s.n + (t.row0 + t.rows - 1) / a.group + 1);
+    t.u0 = begin + head_units;
+    t.u1 = end;
+    if (split) {
+        t.t0 = int(min(int64_t(t.keys), int64_t(max(0, u - t.u0)) << shift));
+        t.t1 = int(min(int64_t(t.keys), int64_t(max(0, next - t.u0)) << shift));
+    } else {
+        t.t0 = 0;
+        t.t1 = t.keys;
+    }
+    t.first = u <= t.u0 && next > t.u0;
+    t.whole = t.first && next == end;
+    return t;
+}
+
+// A warp's walk over its stages of a tile (every kWarps-th) with its ring of items (keys and values
+// of its stages in turn).  begin() looks up the pages and sends for the first items; run() takes
+// them in.  Between the two a block joins the sums of its tile before, while the copies travel.
+template <int DT, int NT>
+struct Walk {
     using S = Shape<DT, NT>;
-    constexpr int kSpan = 16 * S::kSteps;  // keys of a warp's iteration
+    struct Pages {  // lane l has those of the warp's stage base + l
+        int z[2];   // (page, head) of the stage's boxes; -1: none; -2: no page
+        float ks[S::kSteps], vs[S::kSteps];
+    };
+    const KvAttnArgs &a;
+    const CUtensorMap *km, *vm;
+    Smem<DT, NT> &sm;
+    Tile t;
+    Pages cur, next;
+    int mine;        // the warp's stages: warp + i * kWarps
+    int base;        // the stage that lane 0's pages are for
+    int issued;      // items
+    uint32_t item0;  // items of the warp over all tiles before: item x goes to buffer (item0 + x) % kBufs
+
+    __device__ __forceinline__ Walk(const KvAttnArgs &a_, const CUtensorMap *km_, const CUtensorMap *vm_, Smem<DT, NT> &sm_)
+        : a(a_), km(km_), vm(vm_), sm(sm_), mine(0), item0(0)
+    {
+    }
+    __device__ __forceinline__ int box_rows() const { return min(1 << a.page_shift, S::kKeys); }
+    __device__ __forceinline__ bool two() const { return (1 << a.page_shift) < S::kKeys; }  // a stage lies in two pages
+    __device__ __forceinline__ int key_of(int i) const { return t.t0 + (int(threadIdx.x) / 32 + i * kWarps) * S::kKeys; }
+
+    __device__ __forceinline__ void look_up(Pages &p, int i)
+    {
+        const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int key = key_of(i) + x * 16;
+            p.z[x] = -1;
+            if (i < mine && key < t.t1 && (x == 0 || two())) {
+                const int64_t page = kv_page_ok(__ldg(table + (key >> a.page_shift)), a.num_pages);
+                p.z[x] = page < 0 ? -2 : int(page) * a.kv_heads + t.head;
+            }
+        }
+    }
+    __device__ __forceinline__ void look_up_scales(Pages &p)
+    {
+#pragma unroll
+        for (int e = 0; e < S::kSteps; ++e) {
+            const int z = two() && e ? p.z[1] : p.z[0];
+            p.ks[e] = z >= 0 ? __ldg(a.k_scale + z) : 0.f;
+            p.vs[e] = z >= 0 ? __ldg(a.v_scale + z) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void issue()
+    {
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+        const int x = issued++, i = x / 2 - base;
+        const int z0 = __shfl_sync(0xffffffffu, i < 32 ? cur.z[0] : next.z[0], i % 32);
+        const int z1 = __shfl_sync(0xffffffffu, i < 32 ? cur.z[1] : next.z[1], i % 32);
+        if (lane == 0) {
+            const uint32_t b = (item0 + x) % S::kBufs;
+            uint8_t *dst = sm.ring[warp][b];
+            uint64_t *bar = &sm.full[warp][b];
+            const CUtensorMap *map = x & 1 ? vm : km;
+            const uint32_t bytes = uint32_t(box_rows() * S::kRowBytes * S::kBoxes);
+            mbar_arrive_expect_tx(bar, (z0 >= 0 ? bytes : 0u) + (z1 >= 0 ? bytes : 0u));
+            const int y = two() ? 0 : key_of(x / 2) & ((1 << a.page_shift) - 1);
+#pragma unroll
+            for (int c = 0; c < S::kBoxes; ++c) {
+                if (z0 >= 0) tma_load_3d(dst + c * S::kBoxBytes, map, 128 * c, y, z0, bar);
+                if (z1 >= 0) tma_load_3d(dst + c * S::kBoxBytes + 16 * S::kRowBytes, map, 128 * c, 0, z1, bar);
+            }
+            if (z0 == -2 || z1 == -2) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
+        }
+    }
+    __device__ __forceinline__ bool ready(int x)
+    {
+        return wait_warp(&sm.full[threadIdx.x / 32][(item0 + x) % S::kBufs], ((item0 + x) / S::kBufs) & 1, &sm.abort);
+    }
+
+    // All items of the tile before are taken in (the ring is free).
+    __device__ __forceinline__ void begin(const Tile &tile)
+    {
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+        item0 += 2u * uint32_t(mine);
+        t = tile;
+        const int n = (t.t1 - t.t0 + S::kKeys - 1) / S::kKeys;  // stages of the tile
+        mine = max(0, n - warp + kWarps - 1) / kWarps;
+        base = issued = 0;
+        if (mine == 0) return;
+        look_up(cur, lane);
+        look_up_scales(cur);  // in front of the copies, which would delay them
+#pragma unroll 1
+        while (issued < min(int(S::kBufs), 2 * mine)) issue();
+        look_up(next, 32 + lane);
+    }
+    template <bool F8, bool BF16>
+    __device__ __forceinline__ void run(State<DT, NT> &st);
+};
+
+template <int DT, int NT>
+template <bool F8, bool BF16>
+__device__ __forceinline__ void Walk<DT, NT>::run(State<DT, NT> &st)
+{
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, j = lane % 4;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        st.m[n][0] = st.m[n][1] = -INFINITY;
-        st.l[n][0] = st.l[n][1] = 0.f;
+    for (int r = 0; r < NT; ++r) {
+        st.m[r][0] = st.m[r][1] = -INFINITY;
+        st.l[r][0] = st.l[r][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < DT / 16; ++i)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) st.o[n][i][x] = 0.f;
+            for (int x = 0; x < 4; ++x) st.o[r][i][x] = 0.f;
     }
+    if (mine == 0) return;
+    const int items = 2 * mine;
     uint32_t qf[NT][DT / 16][2];
     float qs[NT][2];
     load_queries<BF16, DT, NT>(a, t.s, t.head, t.row0, t.rows, g, j, qf, qs);
     int seen[NT][2];  // keys that rows 2j and 2j + 1 see
-    int least = t1;   // keys that every row of the tile sees
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < NT; ++r)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int r = 8 * n + 2 * j + x;
-            seen[n][x] = r < t.rows ? t.s.len - t.s.n + (t.row0 + r) / a.group + 1 : 0;
-            qs[n][x] *= a.sm_scale * kLog2e;
+            const int row = 8 * r + 2 * j + x;
+            seen[r][x] = row < t.rows ? min(t.t1, t.s.len - t.s.n + (t.row0 + row) / a.group + 1) : 0;
+            qs[r][x] *= a.sm_scale * kLog2e;
         }
-    least = min(least, t.s.len - t.s.n + t.row0 / a.group + 1);
-    const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
-    const int last_page = (t1 - 1) >> a.page_shift;
+    const int least = min(t.t1, t.s.len - t.s.n + t.row0 / a.group + 1);  // keys that every row sees
 
-    KeyRegs<DT> kr[S::kSteps];
-    ValRegs<DT> vr[S::kSteps];
-    float ks[S::kSteps], vs[S::kSteps];
-    int64_t at[S::kSteps];  // byte offset of the step's codes (page 0 for a bad entry)
-    bool ok[S::kSteps];
-    auto page_of = [&](int key) { return table[min(key >> a.page_shift, last_page)]; };
-    auto place = [&](int i, int entry, int key) {
-        const int64_t page = kv_page_ok(entry, a.num_pages);
-        ok[i] = page >= 0;
-        if (!ok[i] && key < t1) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
-        const int64_t p = ok[i] ? page : 0;
-        at[i] = kv_code_offset(p, t.head, key & ((1 << a.page_shift) - 1), a.kv_heads, a.page_shift, a.pitch);
-        const int64_t si = kv_scale_index(p, t.head, a.kv_heads);
-        ks[i] = __ldg(a.k_scale + si);
-        vs[i] = ok[i] ? __ldg(a.v_scale + si) : 0.f;
-    };
-    int key = t0 + warp * kSpan;
-    if (key >= t1) return;
-    int entry[S::kSteps];
-#pragma unroll
-    for (int i = 0; i < S::kSteps; ++i) entry[i] = page_of(key + 16 * i);
-#pragma unroll
-    for (int i = 0; i < S::kSteps; ++i) {
-        place(i, entry[i], key + 16 * i);
-        load_keys<DT>(kr[i], a.k + at[i], a.pitch, g, j);
-    }
-#pragma unroll
-    for (int i = 0; i < S::kSteps; ++i) load_vals<DT>(vr[i], a.v + at[i], a.pitch, g, j);
-    constexpr int kStride = kWarps * kSpan;
-#pragma unroll
-    for (int i = 0; i < S::kSteps; ++i) entry[i] = page_of(key + kStride + 16 * i);
-
-    for (; key < t1; key += kStride) {
-        float s[S::kSteps][NT][4];
-        float vcur[S::kSteps];
-        const bool more = key + kStride < t1;
-#pragma unroll
-        for (int i = 0; i < S::kSteps; ++i) {
-            if (F8 && a.head_dim < a.pitch) {  // bytes behind the head hold anything, NaN codes among it
-#pragma unroll
-                for (int c = 0; c < DT / 64; ++c)
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        if (64 * c + 16 * j + 4 * w >= a.head_dim) (&kr[i].r[0][c].x)[w] = (&kr[i].r[1][c].x)[w] = 0u;
-            }
-            scores<F8, DT, NT>(kr[i], qf, s[i]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[i][n][x] *= ks[i] * qs[n][x & 1];
-            const int first = key + 16 * i;
-            if (first + 16 > least || !ok[i]) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int k = first + g + 8 * (x >> 1);
-                        if (k >= min(seen[n][x & 1], t1) || !ok[i]) s[i][n][x] = -INFINITY;
-                    }
-                // slots behind the last key hold anything, e4m3 NaN codes among it
-                if (F8 && first + 16 > t1) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (first + 2 * j + (c & 1) + 8 * (c >> 1) >= t1)
-#pragma unroll
-                            for (int w = 0; w < DT / 32; ++w) vr[i].w[c][w] = 0u;
-                }
-            }
-            vcur[i] = vs[i];
+    const bool pair = two();
+    int done = 0;  // items waited for
+    for (int i = 0; i < mine; ++i) {
+        if (i - base == 32) {
+            base += 32;
+            cur = next;
+            look_up(next, base + 32 + lane);
         }
-        // the next keys are on their way while the softmax and the values are worked on
-        if (more) {
+        if (i - base == 8) look_up_scales(next);
+        const int key = key_of(i);
+        float s[S::kSteps][NT][4], vs[S::kSteps];
+        const uint8_t *k = sm.ring[warp][(item0 + 2 * i) % S::kBufs], *v = sm.ring[warp][(item0 + 2 * i + 1) % S::kBufs];
+        if (!ready(done++)) break;
 #pragma unroll
-            for (int i = 0; i < S::kSteps; ++i) {
-                place(i, entry[i], key + kStride + 16 * i);
-                load_keys<DT>(kr[i], a.k + at[i], a.pitch, g, j);
-                entry[i] = page_of(key + 2 * kStride + 16 * i);
+        for (int e = 0; e < S::kSteps; ++e) {
+            scores<F8, DT, NT>(k, 16 * e, g, j, qf, s[e]);
+            const float ks = __shfl_sync(0xffffffffu, cur.ks[e], i - base);
+            vs[e] = __shfl_sync(0xffffffffu, cur.vs[e], i - base);
+            const int z = __shfl_sync(0xffffffffu, pair && e ? cur.z[1] : cur.z[0], i - base);
+#pragma unroll
+            for (int r = 0; r < NT; ++r)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[e][r][x] *= ks * qs[r][x & 1];
+            const int first = key + 16 * e;
+            if (first + 16 > least || z < 0) {
+#pragma unroll
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (first + g + 8 * (x >> 1) >= seen[r][x & 1] || z < 0) s[e][r][x] = -INFINITY;
             }
         }
+        __syncwarp();  // the keys are read: their buffer takes the next item
+        if (issued < items) issue();
         uint32_t p[S::kSteps][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float mx[2] = {st.m[n][0], st.m[n][1]};
+        for (int r = 0; r < NT; ++r) {
+            float mx[2] = {st.m[r][0], st.m[r][1]};
 #pragma unroll
-            for (int i = 0; i < S::kSteps; ++i)
+            for (int e = 0; e < S::kSteps; ++e)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mx[x & 1] = fmaxf(mx[x & 1], s[i][n][x]);
+                for (int x = 0; x < 4; ++x) mx[x & 1] = fmaxf(mx[x & 1], s[e][r][x]);
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) {
                 mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
                 mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
             }
-            if (__any_sync(0xffffffffu, mx[0] > st.m[n][0] || mx[1] > st.m[n][1])) {
+            if (__any_sync(0xffffffffu, mx[0] > st.m[r][0] || mx[1] > st.m[r][1])) {
                 // -inf - -inf: no key seen yet, nothing to rescale
-                const float f0 = mx[0] == st.m[n][0] ? 1.f : exp2_approx(st.m[n][0] - mx[0]);
-                const float f1 = mx[1] == st.m[n][1] ? 1.f : exp2_approx(st.m[n][1] - mx[1]);
-                st.l[n][0] *= f0;
-                st.l[n][1] *= f1;
+                const float f0 = mx[0] == st.m[r][0] ? 1.f : exp2_approx(st.m[r][0] - mx[0]);
+                const float f1 = mx[1] == st.m[r][1] ? 1.f : exp2_approx(st.m[r][1] - mx[1]);
+                st.l[r][0] *= f0;
+                st.l[r][1] *= f1;
 #pragma unroll
-                for (int i = 0; i < DT / 16; ++i) {
-                    st.o[n][i][0] *= f0;
-                    st.o[n][i][1] *= f1;
-                    st.o[n][i][2] *= f0;
-                    st.o[n][i][3] *= f1;
+                for (int c = 0; c < DT / 16; ++c) {
+                    st.o[r][c][0] *= f0;
+                    st.o[r][c][1] *= f1;
+                    st.o[r][c][2] *= f0;
+                    st.o[r][c][3] *= f1;
                 }
-                st.m[n][0] = mx[0];
-                st.m[n][1] = mx[1];
+                st.m[r][0] = mx[0];
+                st.m[r][1] = mx[1];
             }
-            const float base[2] = {mx[0] == -INFINITY ? 0.f : mx[0] - kRaise, mx[1] == -INFINITY ? 0.f : mx[1] - kRaise};
+            const float low[2] = {mx[0] == -INFINITY ? 0.f : mx[0] - kRaise, mx[1] == -INFINITY ? 0.f : mx[1] - kRaise};
 #pragma unroll
-            for (int i = 0; i < S::kSteps; ++i) {
+            for (int e = 0; e < S::kSteps; ++e) {
                 float w[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    w[x] = exp2_approx(s[i][n][x] - base[x & 1]);
-                    st.l[n][x & 1] += w[x];
+                    w[x] = exp2_approx(s[e][r][x] - low[x & 1]);
+                    st.l[r][x & 1] += w[x];
                 }
                 // weights to binary16: half a step is 2^-12 of each, of either sign
-                p[i][n][0] = trans8x8(act_t2<__half>(w[0], w[1]));
-                p[i][n][1] = trans8x8(act_t2<__half>(w[2], w[3]));
+                p[e][r][0] = trans8x8(act_t2<__half>(w[0], w[1]));
+                p[e][r][1] = trans8x8(act_t2<__half>(w[2], w[3]));
             }
         }
+        if (!ready(done++)) break;
 #pragma unroll
-        for (int i = 0; i < S::kSteps; ++i) {
-            add_values<F8, DT, NT>(vr[i], p[i], vcur[i], st);
-            if (more) load_vals<DT>(vr[i], a.v + at[i], a.pitch, g, j);
+        for (int e = 0; e < S::kSteps; ++e) {
+            const int z = __shfl_sync(0xffffffffu, pair && e ? cur.z[1] : cur.z[0], i - base);
+            add_values<F8, DT, NT>(v, 16 * e, z < 0 ? 0 : t.t1 - (key + 16 * e), g, j, p[e], vs[e], st);
         }
+        __syncwarp();
+        if (issued < items) issue();
+    }
+    // (only after a wait gave up: nothing may land in memory that is used for something else)
+    while (done < issued) ready(done++);
+}
+
+__device__ __forceinline__ uint16_t *out_row(const KvAttnArgs &a, const Tile &t, int r)
+{
+    const int row = t.row0 + r;
+    return static_cast<uint16_t *>(a.out) +
+           (int64_t(t.s.q0 + row / a.group) * a.q_heads + t.head * a.group + row % a.group) * a.head_dim;
+}
+__device__ __forceinline__ float inverse_of(float l) { return l > 0.f ? 1.f / l : (l == l ? 0.f : l); }
+__device__ __forceinline__ float weight_of(float m, float top) { return m == -INFINITY ? 0.f : exp2_approx(m - top); }
+
+// The warps' states of a tile joined, a quarter of the places at a time: finished rows, or this
+// block's partial in `slot`.
+template <typename T, int DT, int NT>
+__device__ __forceinline__ void join(const KvAttnArgs &a, Smem<DT, NT> &sm, const Tile &t, State<DT, NT> &st, float *slot)
+{
+    using S = Shape<DT, NT>;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, j = lane % 4;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+            st.l[n][0] += __shfl_xor_sync(0xffffffffu, st.l[n][0], o);
+            st.l[n][1] += __shfl_xor_sync(0xffffffffu, st.l[n][1], o);
+        }
+        if (g == 0) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                sm.m[warp][8 * n + 2 * j + x] = st.m[n][x];
+                sm.l[warp][8 * n + 2 * j + x] = st.l[n][x];
+            }
+        }
+    }
+    constexpr int kQuarter = DT / 4, kPairs = kQuarter / 2;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < DT / 64; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    *reinterpret_cast<float2 *>(&sm.o[warp][8 * n + 2 * j + x][16 * i + 2 * g]) =
+                        make_float2(st.o[n][h * (DT / 64) + i][x], st.o[n][h * (DT / 64) + i][2 + x]);
+        __syncthreads();
+        if (h == 0) {
+            if (tid < S::kRows) {
+                float m = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][tid]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = weight_of(sm.m[w][tid], m);
+                    sm.f[w][tid] = f;
+                    l += f * sm.l[w][tid];
+                }
+                sm.top[tid] = m;
+                sm.weight[tid] = l;
+                if (slot && tid < t.rows) *reinterpret_cast<float2 *>(slot + tid * S::kRowFloats + DT) = make_float2(m, l);
+            }
+            __syncthreads();
+        }
+        for (int e = tid; e < t.rows * kPairs; e += kThreads) {
+            const int r = e / kPairs, at = 2 * (e % kPairs), place = h * kQuarter + at;
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 v = *reinterpret_cast<const float2 *>(&sm.o[w][r][at]);
+                x += sm.f[w][r] * v.x;
+                y += sm.f[w][r] * v.y;
+            }
+            if (slot) {
+                *reinterpret_cast<float2 *>(slot + r * S::kRowFloats + place) = make_float2(x, y);
+            } else {
+                const float inv = inverse_of(sm.weight[r]);
+                const int d = dim_of<DT>(place);
+                if (d < a.head_dim) *reinterpret_cast<uint32_t *>(out_row(a, t, r) + d) = act_t2<T>(x * inv, y * inv);
+            }
+        }
+        __syncthreads();
     }
 }
 
-template <bool F8, bool BF16, int DT, int NT>
-__global__ void __launch_bounds__(kThreads, DT >= 256 || NT > 1 ? 2 : 3)
-kv_attn_rows_kernel(const __grid_constant__ KvAttnArgs a)
+// Joins the partials of a tile: those of `parts` blocks from p0 on (its second slot, the others'
+// first), in the order of their keys.
+template <typename T, int DT, int NT>
+__device__ __forceinline__ void join_parts(const KvAttnArgs &a, const Tile &t, const float *p0, int parts)
 {
     using S = Shape<DT, NT>;
-    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<DT, NT> &sm = *reinterpret_cast<Smem<DT, NT> *>(smem_raw);
-    int64_t *before = reinterpret_cast<int64_t *>(smem_raw + sizeof(Smem<DT, NT>));  // units of sequences < b
+    constexpr int kQuads = DT / 4, kSlot = S::kRows * S::kRowFloats;
+    constexpr int kBatch = 8;  // parts whose loads are in flight together
+#pragma unroll 1
+    for (int e = threadIdx.x; e < t.rows * kQuads; e += kThreads) {
+        const int r = e / kQuads, place = 4 * (e % kQuads);
+        float m = -INFINITY, l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int c0 = 0; c0 < parts; c0 += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int c = min(c0 + i, parts - 1);
+                const float *row = p0 + c * (2 * kSlot) + (c == 0 ? kSlot : 0) + r * S::kRowFloats;
+                ml[i] = __ldcg(reinterpret_cast<const float2 *>(row + DT));
+                v[i] = __ldcg(reinterpret_cast<const float4 *>(row + place));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (c0 + i >= parts) break;
+                const float top = fmaxf(m, ml[i].x), f = weight_of(m, top), w = weight_of(ml[i].x, top);
+                l = f * l + w * ml[i].y;
+                x.x = f * x.x + w * v[i].x;
+                x.y = f * x.y + w * v[i].y;
+                x.z = f * x.z + w * v[i].z;
+                x.w = f * x.w + w * v[i].w;
+                m = top;
+            }
+        }
+        uint16_t *out = out_row(a, t, r);
+        const float inv = inverse_of(l);
+        const int d0 = dim_of<DT>(place), d1 = dim_of<DT>(place + 2);
+        if (d0 < a.head_dim) *reinterpret_cast<uint32_t *>(out + d0) = act_t2<T>(x.x * inv, x.y * inv);
+        if (d1 < a.head_dim) *reinterpret_cast<uint32_t *>(out + d1) = act_t2<T>(x.z * inv, x.w * inv);
+    }
+}
+
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
+// kv_share in 32 bits (total and grid * grid fit).
+__device__ __forceinline__ int share_of(int total, int c, int grid)
+{
+    const unsigned q = unsigned(total) / unsigned(grid), r = unsigned(total) % unsigned(grid);
+    return int(q * unsigned(c) + r * unsigned(c) / unsigned(grid));
+}
+
+template <bool F8, bool BF16, int DT, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<DT, NT>::kPerSm)
+kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                    const __grid_constant__ KvAttnArgs a)
+{
+    using S = Shape<DT, NT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem<DT, NT> &sm = *reinterpret_cast<Smem<DT, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int *before = reinterpret_cast<int *>(&sm + 1);  // units of sequences < b
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.full[w][i], 1);
+        sm.abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&km);
+        tma_prefetch_desc(&vm);
+    }
     grid_dep_launch();
     grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
 
     // units of every sequence, summed up: each thread takes a run of sequences
     const bool split = a.partials != nullptr;
     const int per = (a.n_seqs + kThreads - 1) / kThreads;
+    int shift = kUnitShift;
     auto units_of = [&](int b) {
         const int len = a.seq_len[b];
         const KvSpan s = kv_span(a.cu_q[b], a.cu_q[b + 1], len, a.M, a.capacity);
         if (len > a.capacity) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
         if (int64_t(s.n) * a.group > a.few_rows) return int64_t(0);
-        return kv_tiles(s.n, a.group, S::kRows) * (split ? kv_units(s.len, kUnit) : 1) * a.kv_heads;
+        return kv_tiles(s.n, a.group, S::kRows) * a.kv_heads * (split ? kTileUnits + kv_units(s.len, 1 << shift) : 1);
     };
-    int64_t mine = 0;
-    for (int i = 0; i < per; ++i)
-        if (tid * per + i < a.n_seqs) mine += units_of(tid * per + i);
-    int64_t sum = mine;
+    int64_t mine, sum, all;
+    for (;; ++shift) {  // (larger units where their count would not fit: more than 2^36 keys)
+        mine = 0;
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < a.n_seqs) mine += units_of(tid * per + i);
+        sum = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) sm.sums[warp] = sum;
+        __syncthreads();
+        all = 0;
+        int64_t below = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) below += sm.sums[w];
+            all += sm.sums[w];
+        }
+        sum += below - mine;
+        if (all <= kMostUnits || shift == 30) break;
+        __syncthreads();
     }
-    if (lane == 31) sm.sums[warp] = sum;
-    __syncthreads();
-    int64_t run = sum - mine, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) run += sm.sums[w];
-        total += sm.sums[w];
-    }
+    const int total = int(min(all, int64_t(0x7fffffff)));
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b < a.n_seqs) {
-            before[b] = run;
-            run += per > 1 ? units_of(b) : mine;
+            before[b] = int(sum);
+            sum += per > 1 ? units_of(b) : mine;
         }
     }
     if (tid == 0) before[a.n_seqs] = total;
     __syncthreads();
 
     // no more shares than units, so that no block between a tile's first and last is without one
-    const int grid = int(min(int64_t(gridDim.x), total)), cta = blockIdx.x;
+    const int least = split ? kTileUnits + kLeastUnits : 1;
+    const int grid = min(int(gridDim.x), (total + least - 1) / least), cta = blockIdx.x;
     if (cta >= grid) return;
-    int64_t u = kv_share(total, cta, grid);
-    const int64_t u_end = kv_share(total, cta + 1, grid);
-    while (u < u_end) {
-        // the sequence of unit u: the last b with before[b] <= u (empty ones have no units)
-        int lo = 0, hi = a.n_seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (before[mid] <= u) lo = mid;
-            else hi = mid;
+    int u = share_of(total, cta, grid);
+    const int u_end = share_of(total, cta + 1, grid);
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    constexpr int kSlot = S::kRows * S::kRowFloats;
+    // the block's next part of a tile (u: the unit behind it)
+    auto next_part = [&](Tile &t) {
+        while (u < u_end) {
+            int next;
+            t = tile_of<S::kRows>(a, before, shift, u, u_end, next);
+            u = next;
+            if (next > t.u0) return true;  // (else none of the tile's keys)
         }
-        Tile t;
-        t.b = lo;
-        t.s = kv_span(a.cu_q[lo], a.cu_q[lo + 1], a.seq_len[lo], a.M, a.capacity);
-        const int64_t units = split ? kv_units(t.s.len, kUnit) : 1;
-        const int64_t tiles = kv_tiles(t.s.n, a.group, S::kRows);
-        const int64_t item = (u - before[lo]) / units;  // (key head, tile) of the sequence
-        const int64_t item_u0 = before[lo] + item * units;
-        t.head = int(item / tiles);
-        t.row0 = int(item % tiles) * S::kRows;
-        t.rows = min(S::kRows, t.s.n * a.group - t.row0);
-        t.keys = max(0, t.s.len - t.s.n + (t.row0 + t.rows - 1) / a.group + 1);
-        const int64_t item_end = item_u0 + units, seg_end = min(item_end, u_end);
-        // keys of this block's units of the tile
-        const int t0 = split ? int(min(int64_t(t.keys), (u - item_u0) * kUnit)) : 0;
-        const int t1 = split ? int(min(int64_t(t.keys), (seg_end - item_u0) * kUnit)) : t.keys;
-        const bool whole = u == item_u0 && seg_end == item_end;
-
+        return false;
+    };
+    Walk<DT, NT> walk(a, &km, &vm, sm);
+    Tile t, ahead, kept[2];
+    bool kept_any[2] = {false, false};  // partials of a tile that began before, of one that ends behind
+    bool more = next_part(t);
+    if (more) walk.begin(t);
+#pragma unroll 1
+    while (more) {
         State<DT, NT> st;
-        walk_keys<F8, BF16, DT, NT>(a, t, t0, t1, st);
-
-        // the warps' states, joined in shared memory
-        const int g = lane / 4, j = lane % 4;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                st.l[n][0] += __shfl_xor_sync(0xffffffffu, st.l[n][0], o);
-                st.l[n][1] += __shfl_xor_sync(0xffffffffu, st.l[n][1], o);
-            }
-            if (g == 0) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    sm.m[warp][8 * n + 2 * j + x] = st.m[n][x];
-                    sm.l[warp][8 * n + 2 * j + x] = st.l[n][x];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < DT / 16; ++i)
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    *reinterpret_cast<float2 *>(&sm.o[warp][8 * n + 2 * j + x][16 * i + 2 * g]) =
-                        make_float2(st.o[n][i][x], st.o[n][i][2 + x]);
+        walk.template run<F8, BF16>(st);
+        more = next_part(ahead);
+        if (more) walk.begin(ahead);
+        float *slot = t.whole ? nullptr : a.partials + int64_t(2 * cta + (t.first ? 1 : 0)) * kSlot;
+        join<T, DT, NT>(a, sm, t, st, slot);
+        if (!t.whole) {
+            if (t.first) kept[1] = t;
+            else kept[0] = t;
+            kept_any[t.first] = true;
         }
-        __syncthreads();
-        // partial of this block, or the finished rows
-        float *slot = nullptr;
-        if (!whole) slot = a.partials + int64_t(2 * cta + (u == item_u0 ? 1 : 0)) * S::kRows * S::kRowFloats;
-        for (int e = tid; e < S::kRows * (DT / 2); e += kThreads) {
-            const int r = e / (DT / 2), at = 2 * (e % (DT / 2)), d = dim_of<DT>(at);
-            float m = sm.m[0][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm.m[w][r]);
-            float l = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = sm.m[w][r];
-                const float f = mw == -INFINITY ? 0.f : exp2_approx(mw - m);
-                l += f * sm.l[w][r];
-                x += f * sm.o[w][r][at];
-                y += f * sm.o[w][r][at + 1];
-            }
-            if (whole) {
-                if (r < t.rows && d < a.head_dim) {
-                    const int row = t.row0 + r;
-                    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-                    uint16_t *o = static_cast<uint16_t *>(a.out) +
-                                  (int64_t(t.s.q0 + row / a.group) * a.q_heads + t.head * a.group + row % a.group) *
-                                      a.head_dim + d;
-                    *reinterpret_cast<uint32_t *>(o) = act_t2<T>(x * inv, y * inv);
-                }
-            } else {
-                *reinterpret_cast<float2 *>(slot + r * S::kRowFloats + at) = make_float2(x, y);
-                if (at == 0) *reinterpret_cast<float2 *>(slot + r * S::kRowFloats + DT) = make_float2(m, l);
-            }
-        }
-        if (!whole) {
-            // the blocks of a tile arrive at the counter of the tile's first block
-            const int c0 = [&] {
-                int x = int(item_u0 * grid / total);  // near the block that holds unit item_u0
-                while (x > 0 && kv_share(total, x, grid) > item_u0) --x;
-                while (kv_share(total, x + 1, grid) <= item_u0) ++x;
-                return x;
-            }();
-            const int c1 = [&] {
-                int x = int((item_end - 1) * grid / total);
-                while (x > 0 && kv_share(total, x, grid) > item_end - 1) --x;
-                while (kv_share(total, x + 1, grid) <= item_end - 1) ++x;
-                return x;
-            }();
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) sm.last = atomicInc(&a.arrivals[c0], unsigned(c1 - c0)) == unsigned(c1 - c0);
-            __syncthreads();
-            if (sm.last) {
-                __threadfence();
-                const int64_t stride = int64_t(2) * S::kRows * S::kRowFloats;
-                const float *p0 = a.partials + int64_t(c0) * stride;  // its second slot, the others' first
-                auto part = [&](int c) { return p0 + (c - c0) * stride + (c == c0 ? S::kRows * S::kRowFloats : 0); };
-                for (int e = tid; e < t.rows * (DT / 2); e += kThreads) {
-                    const int r = e / (DT / 2), at = 2 * (e % (DT / 2)), d = dim_of<DT>(at);
-                    if (d >= a.head_dim) continue;
-                    float m = -INFINITY;
-                    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part(c) + r * S::kRowFloats + DT));
-                    float l = 0.f, x = 0.f, y = 0.f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float *row = part(c) + r * S::kRowFloats;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(row + DT));
-                        const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
-                        const float2 xy = __ldcg(reinterpret_cast<const float2 *>(row + at));
-                        l += f * ml.y;
-                        x += f * xy.x;
-                        y += f * xy.y;
-                    }
-                    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-                    const int row = t.row0 + r;
-                    uint16_t *out = static_cast<uint16_t *>(a.out) +
-                                    (int64_t(t.s.q0 + row / a.group) * a.q_heads + t.head * a.group + row % a.group) *
-                                        a.head_dim + d;
-                    *reinterpret_cast<uint32_t *>(out) = act_t2<T>(x * inv, y * inv);
-                }
-            }
-        }
-        __syncthreads();  // shared memory is reused by the next tile
-        u = seg_end;
+        t = ahead;
     }
+    // Every partial of the block is written: it arrives at the counters of their tiles (of the
+    // tile's first block), and joins the parts of those that it is the last to arrive at.
+    if (!kept_any[0] && !kept_any[1]) return;
+    if (tid == 0) {
+        auto owner = [&](int x) {
+            int c = int(unsigned(int64_t(x) * grid / total));  // at or next to the block that holds unit x
+            while (c > 0 && share_of(total, c, grid) > x) --c;
+            while (share_of(total, c + 1, grid) <= x) ++c;
+            return c;
+        };
+        int c0[2], parts[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (kept_any[i]) {
+                c0[i] = i ? cta : owner(kept[i].u0);
+                parts[i] = (i ? owner(kept[i].u1 - 1) : (kept[i].u1 - 1 < u_end ? cta : owner(kept[i].u1 - 1))) - c0[i] + 1;
+            }
+        fence_gpu();  // the block's partials, seen by this thread at the barrier, before its arrivals
+        bool last[2] = {false, false};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (kept_any[i]) last[i] = atomicInc(&a.arrivals[c0[i]], unsigned(parts[i] - 1)) == unsigned(parts[i] - 1);
+        if (last[0] || last[1]) fence_gpu();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sm.first[i] = last[i] ? c0[i] : 0;
+            sm.parts[i] = last[i] ? parts[i] : 0;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (kept_any[i] && sm.parts[i])
+            join_parts<T, DT, NT>(a, kept[i], a.partials + int64_t(sm.first[i]) * (2 * kSlot), sm.parts[i]);
 }
 
 struct RowsPlan {
     const void *fn;
-    int per_sm;      // resident blocks
-    size_t smem;     // without the unit counts
+    int per_sm;
+    size_t smem;    // without the unit counts
+    int row_bytes;  // of a copied box
+    int keys;       // of a stage
 };
 
-template <bool F8, bool BF16, int DT>
-RowsPlan rows_plan(bool two)
+template <bool F8, bool BF16, int DT, int NT>
+RowsPlan rows_plan()
 {
-    if (two)
-        return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, DT, 2>), 2, sizeof(Smem<DT, 2>)};
-    return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, DT, 1>), DT >= 256 ? 2 : 3, sizeof(Smem<DT, 1>)};
+    using S = Shape<DT, NT>;
+    return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, DT, NT>), S::kPerSm,
+            sizeof(Smem<DT, NT>) + 1024, S::kRowBytes, S::kKeys};
 }
 
 template <bool F8, bool BF16>
 RowsPlan rows_plan(int head_dim, bool two)
 {
-    if (head_dim <= 64) return rows_plan<F8, BF16, 64>(two);
-    if (head_dim <= 128) return rows_plan<F8, BF16, 128>(two);
-    return rows_plan<F8, BF16, 256>(two);
+    if (head_dim <= 64) return two ? rows_plan<F8, BF16, 64, 2>() : rows_plan<F8, BF16, 64, 1>();
+    if (head_dim <= 128) return two ? rows_plan<F8, BF16, 128, 2>() : rows_plan<F8, BF16, 128, 1>();
+    return two ? rows_plan<F8, BF16, 256, 2>() : rows_plan<F8, BF16, 256, 1>();
 }
 
-constexpr int kMostPerSm = 3;
+constexpr int kMostPerSm = 2;
 constexpr int kFewRows = 16;
-// two partial slots a block: the largest of 3 blocks of 8 rows of 130 binary32 values, 2 blocks
-// of 16 rows of 258
-static_assert(3 * 2 * 8 * (128 + 2) * 4 <= 65536 && 2 * 2 * 16 * (256 + 2) * 4 <= 2 * 65536, "");
+// two partial slots a block in the workspace's 64 KB per SM: two blocks of 8 rows of 132 binary32
+// values, or one of 16 rows of 260
+static_assert(2 * 2 * 8 * (128 + 4) * 4 <= 65536 && 2 * 16 * (256 + 4) * 4 <= 65536, "");
 
 }  // namespace
 
 // Partials of two slots for every block, then the arrival counters (self-resetting).
-static size_t rows_partial_bytes() { return size_t(device_info().sm_count) * 2 * 2 * 16 * (256 + 2) * 4; }
-
 size_t kv_attn_rows_workspace()
 {
-    return std::max(rows_partial_bytes(), ws_scratch_bytes()) + size_t(device_info().sm_count) * kMostPerSm * sizeof(unsigned);
+    return ws_scratch_bytes() + size_t(device_info().sm_count) * kMostPerSm * sizeof(unsigned);
 }
 
 wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
@@ -653,11 +868,29 @@ wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
     const bool two = int64_t(a.M) * a.group > int64_t(8) * a.n_seqs;
     const RowsPlan p = f8 ? (bf16 ? rows_plan<true, true>(a.head_dim, two) : rows_plan<true, false>(a.head_dim, two))
                           : (bf16 ? rows_plan<false, true>(a.head_dim, two) : rows_plan<false, false>(a.head_dim, two));
-    const size_t smem = p.smem + size_t(a.n_seqs + 1) * sizeof(int64_t);
-    if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem + (kKvMaxSeqs + 1) * 8)) != cudaSuccess)
+    const size_t smem = p.smem + size_t(a.n_seqs + 1) * sizeof(int);
+    if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem + (kKvMaxSeqs + 1) * sizeof(int))) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_rows_kernel)");
+    CUtensorMap km, vm;
+    // bytes behind the head are not read: the copy fills zeros beyond the first dimension
+    const uint64_t dims[3] = {uint64_t(a.head_dim), uint64_t(1) << a.page_shift, uint64_t(a.num_pages) * a.kv_heads};
+    const uint64_t strides[2] = {uint64_t(a.pitch), uint64_t(a.pitch) << a.page_shift};
+    const uint32_t box[3] = {uint32_t(p.row_bytes), uint32_t(std::min(1 << a.page_shift, p.keys)), 1};
+    wq_status rc = encode_tmap(&km, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.k, dims, strides, box, p.row_bytes);
+    if (rc != WQ_OK) return rc;
+    rc = encode_tmap(&vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.v, dims, strides, box, p.row_bytes);
+    if (rc != WQ_OK) return rc;
     PreparedLaunch L;
-    L.set(p.fn, dim3(unsigned(device_info().sm_count * p.per_sm)), dim3(kThreads), smem, a);
+    L.func = p.fn;
+    L.grid = dim3(unsigned(device_info().sm_count * p.per_sm));
+    L.block = dim3(kThreads);
+    L.smem = smem;
+    static_assert(sizeof(CUtensorMap) == 128 && sizeof(KvAttnArgs) <= 256, "argument layout");
+    memcpy(L.args, &km, sizeof km);
+    memcpy(L.args + 128, &vm, sizeof vm);
+    memcpy(L.args + 256, &a, sizeof a);
+    for (int i = 0; i < 3; ++i) L.argp[i] = L.args + 128 * i;
+    L.nargs = 3;
     return launch_prepared(L, st, "kv_attn_rows_kernel");
 }
 
@@ -704,11 +937,9 @@ extern "C" wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t
     a.pitch = kv_pitch(cache->head_dim);
     a.capacity = int(batch->max_pages * cache->page_size);
     a.sm_scale = sm_scale;
-    const size_t need = kv_attn_rows_workspace();
-    if (workspace && ws_bytes >= need) {
+    if (workspace && ws_bytes >= kv_attn_rows_workspace()) {
         a.partials = static_cast<float *>(workspace);
-        a.arrivals = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) +
-                                                  std::max(rows_partial_bytes(), ws_scratch_bytes()));
+        a.arrivals = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) + ws_scratch_bytes());
     }
     // Sequences with up to kFewRows rows per key head are bound by reading their keys once and go
     // to the key-split kernel, the others to the tile kernel (heads up to 128).  One launch

@@ -173,7 +173,7 @@ def test_norm_refusals(lib):
 
 CACHE_BAD = [
     (dict(k=None), "INVALID_ARG"), (dict(v_scale=None), "INVALID_ARG"), (dict(num_pages=0), "INVALID_ARG"),
-    (dict(num_pages=2 ** 31), "INVALID_ARG"), (dict(page_size=8), "UNSUPPORTED"), (dict(page_size=48), "UNSUPPORTED"),
+    (dict(num_pages=2 ** 30), "INVALID_ARG"), (dict(page_size=8), "UNSUPPORTED"), (dict(page_size=48), "UNSUPPORTED"),
     (dict(page_size=512), "UNSUPPORTED"), (dict(head_dim=12), "UNSUPPORTED"), (dict(head_dim=130), "UNSUPPORTED"),
     (dict(head_dim=260), "UNSUPPORTED"), (dict(kv_heads=0), "INVALID_ARG"), (dict(kv_heads=3), "INVALID_ARG"),
     (dict(format=wq.FMT_E2M1), "INVALID_ARG"), (dict(k=0x10008), "ALIGNMENT"), (dict(k_scale=0x10002), "ALIGNMENT")]
