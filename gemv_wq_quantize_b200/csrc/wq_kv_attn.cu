@@ -862,6 +862,32 @@ size_t kv_attn_rows_workspace()
     return ws_scratch_bytes() + size_t(device_info().sm_count) * kMostPerSm * sizeof(unsigned);
 }
 
+// Keys and values as (page and head, slot, byte): bytes behind the head are not read, the copy
+// fills zeros beyond the first dimension.
+wq_status encode_cache(CUtensorMap *km, CUtensorMap *vm, const KvAttnArgs &a, int row_bytes, int rows)
+{
+    const uint64_t dims[3] = {uint64_t(a.head_dim), uint64_t(1) << a.page_shift, uint64_t(a.num_pages) * a.kv_heads};
+    const uint64_t strides[2] = {uint64_t(a.pitch), uint64_t(a.pitch) << a.page_shift};
+    const uint32_t box[3] = {uint32_t(row_bytes), uint32_t(rows), 1};
+    wq_status rc = encode_tmap(km, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.k, dims, strides, box, row_bytes);
+    return rc != WQ_OK ? rc : encode_tmap(vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.v, dims, strides, box, row_bytes);
+}
+
+void set_attn_launch(PreparedLaunch &L, const void *fn, unsigned blocks, int threads, size_t smem, const CUtensorMap &km,
+                     const CUtensorMap &vm, const KvAttnArgs &a)
+{
+    static_assert(sizeof(CUtensorMap) == 128 && sizeof(KvAttnArgs) <= 256, "argument layout");
+    L.func = fn;
+    L.grid = dim3(blocks);
+    L.block = dim3(unsigned(threads));
+    L.smem = smem;
+    memcpy(L.args, &km, sizeof km);
+    memcpy(L.args + 128, &vm, sizeof vm);
+    memcpy(L.args + 256, &a, sizeof a);
+    for (int i = 0; i < 3; ++i) L.argp[i] = L.args + 128 * i;
+    L.nargs = 3;
+}
+
 wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
 {
     // 16 rows a tile where sequences bring more than 8 rows per key head on average
@@ -872,25 +898,10 @@ wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
     if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem + (kKvMaxSeqs + 1) * sizeof(int))) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_rows_kernel)");
     CUtensorMap km, vm;
-    // bytes behind the head are not read: the copy fills zeros beyond the first dimension
-    const uint64_t dims[3] = {uint64_t(a.head_dim), uint64_t(1) << a.page_shift, uint64_t(a.num_pages) * a.kv_heads};
-    const uint64_t strides[2] = {uint64_t(a.pitch), uint64_t(a.pitch) << a.page_shift};
-    const uint32_t box[3] = {uint32_t(p.row_bytes), uint32_t(std::min(1 << a.page_shift, p.keys)), 1};
-    wq_status rc = encode_tmap(&km, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.k, dims, strides, box, p.row_bytes);
-    if (rc != WQ_OK) return rc;
-    rc = encode_tmap(&vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.v, dims, strides, box, p.row_bytes);
+    wq_status rc = encode_cache(&km, &vm, a, p.row_bytes, std::min(1 << a.page_shift, p.keys));
     if (rc != WQ_OK) return rc;
     PreparedLaunch L;
-    L.func = p.fn;
-    L.grid = dim3(unsigned(device_info().sm_count * p.per_sm));
-    L.block = dim3(kThreads);
-    L.smem = smem;
-    static_assert(sizeof(CUtensorMap) == 128 && sizeof(KvAttnArgs) <= 256, "argument layout");
-    memcpy(L.args, &km, sizeof km);
-    memcpy(L.args + 128, &vm, sizeof vm);
-    memcpy(L.args + 256, &a, sizeof a);
-    for (int i = 0; i < 3; ++i) L.argp[i] = L.args + 128 * i;
-    L.nargs = 3;
+    set_attn_launch(L, p.fn, unsigned(device_info().sm_count * p.per_sm), kThreads, smem, km, vm, a);
     return launch_prepared(L, st, "kv_attn_rows_kernel");
 }
 

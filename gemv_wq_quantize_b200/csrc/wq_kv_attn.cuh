@@ -23,6 +23,12 @@ struct KvAttnArgs {
     unsigned *arrivals;
 };
 
+// The cache's codes as tensor maps of boxes of `rows` keys by row_bytes (64 or 128, swizzled as
+// wide), and a launch with (key map, value map, arguments).
+wq_status encode_cache(CUtensorMap *km, CUtensorMap *vm, const KvAttnArgs &a, int row_bytes, int rows);
+void set_attn_launch(PreparedLaunch &L, const void *fn, unsigned blocks, int threads, size_t smem, const CUtensorMap &km,
+                     const CUtensorMap &vm, const KvAttnArgs &a);
+
 // Few rows per key head: split over the whole GPU by key ranges (wq_kv_attn.cu).
 wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st);
 size_t kv_attn_rows_workspace();

@@ -14,14 +14,15 @@
 //    the A operand of the second product.  O stays in Tensor Memory; it is rescaled only when the
 //    maximum rose by more than 2^kSlack or a larger value scale arrived, which is rare after the
 //    first blocks.
-//  * warps 8-15: codes of the next block from global memory (in flight in registers while the
-//    block before is worked on), widened to binary16 into the 128-byte swizzled layout of the
-//    MMA's K-major operands: keys as rows of dimensions, values transposed as rows of keys.
-//  * warp 16: one thread issues the MMAs.
+//  * warps 8-11: codes widened to binary16 into the 128-byte swizzled layout of the MMA's K-major
+//    operands: keys as rows of dimensions, values transposed as rows of keys.
+//  * warp 12: one thread issues the MMAs.
+//  * warp 13: brings the next block's codes into shared memory (TMA) and its scales.
 // Every wait is bounded; on expiry the block records an error, stops and frees its Tensor Memory.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "wq_act.cuh"
@@ -46,9 +47,37 @@ constexpr int kTile = 128;           // rows of a tile: MMA M
 constexpr int kRows = 2 * kTile;     // rows of a block
 constexpr int kKeys = 128;           // keys of a step
 constexpr int kGroups = kKeys / 16;  // a group of 16 keys lies in one page
-constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kSoftWarps = 8, kConvWarps = 4;  // (14 warps leave 128 registers a thread)
 constexpr int kConvThreads = 32 * kConvWarps;
-constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
+__device__ __forceinline__ float log2_approx(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t x, y, z, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    memcpy(&z, &c, 8);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    memcpy(&a, &d, 8);
+    return a;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    memcpy(&a, &d, 8);
+    return a;
+}
+
 constexpr int kRing = 4;             // scale sets: a set is rewritten once both tiles are two steps on
 constexpr uint32_t kTmemCols = 512, kScol = 0, kOcol = 256;  // two 128-column tiles of each
 
@@ -57,11 +86,16 @@ constexpr uint32_t kTmemCols = 512, kScol = 0, kOcol = 256;  // two 128-column t
 constexpr float kSlack = 4.f, kRaise = 11.f;
 
 struct Bars {
-    uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], sc_full[kRing], fin;
+    uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], sc_full[kRing];
+    uint64_t raw_k_full, raw_k_free, raw_v_full, raw_v_free, fin;
 };
 struct Scales {
-    float k[kRing][kGroups], v[kRing][kGroups];
-    uint32_t dead[kRing];  // groups whose block-table entry is no page
+    float k[kRing][kGroups];       // key scale * |sm_scale| * log2 e
+    float v[kRing][kGroups];       // value scale, its logarithm and inverse
+    float log_v[kRing][kGroups], inv_v[kRing][kGroups];
+    float v_max[kRing];
+    uint32_t dead[kRing];          // groups whose block-table entry is no page
+    int plain[kRing];              // no dead groups, all value scales positive normal numbers
 };
 
 template <int DT>
@@ -69,7 +103,8 @@ struct Layout {
     static constexpr int kAtom = 128 * 128;            // 128 rows of 64 binary16
     static constexpr int kQ = DT / 64 * kAtom;         // a query tile, a key step
     static constexpr int kV = 2 * DT * 128;            // DT rows of 128 keys
-    static constexpr int kBytes = 2 * kQ + 2 * kQ + 2 * kV;
+    static constexpr int kRaw = kKeys * 128;           // codes of a key step, 128 bytes a key
+    static constexpr int kBytes = 2 * kQ + 2 * kQ + 2 * kV + 2 * kRaw;
 };
 
 __device__ __forceinline__ uint64_t globaltimer()
@@ -79,7 +114,7 @@ __device__ __forceinline__ uint64_t globaltimer()
     return t;
 }
 
-// Waits at most about 2 s, or until another role gave up.  wait_warp: the whole warp, with one
+// Waits at most about 2 s, or 20 ms once another role gave up.  wait_warp: the whole warp, with one
 // answer, so that a warp gives up together.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
@@ -89,8 +124,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait_short(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer() - t0 > 2000000000ull) {
+        if (globaltimer() - t0 > (*abort ? 20000000ull : 2000000000ull)) {
             atomicCAS(&g_kv_tiles_error, kErrNone, kErrWaitTimeout);
             *abort = 1;
             return false;
@@ -103,9 +137,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
-__device__ __forceinline__ uint32_t ldg32(const uint8_t *p) { return __ldg(reinterpret_cast<const uint32_t *>(p)); }
-__device__ __forceinline__ uint4 ldg128(const uint8_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
-
 struct Item {
     KvSpan s;
     int b, head, row0, rows;  // the block's rows
@@ -113,88 +144,100 @@ struct Item {
     int steps, tiles;
 };
 
+// ------------------------------------------------------------------ codes to shared memory
+// A step's codes arrive as one box per page part, 128 bytes a key (zeros behind the head), in the
+// 128-byte swizzle; lanes look up a page each.  Lanes 0 .. 7 also bring a group's scales.
+__device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, const CUtensorMap *km, const CUtensorMap *vm,
+                                          uint8_t *kraw, uint8_t *vraw, Scales &sc, Bars &bar, volatile int *abort)
+{
+    const int lane = threadIdx.x % 32;
+    const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
+    const int box_rows = min(1 << a.page_shift, kKeys), boxes = kKeys / box_rows;
+    // lane l: the page of box l, lane 8 + l: that of group l
+    const int my_key = lane < kGroups ? lane * box_rows : (lane - kGroups) * 16;
+    const bool boxed = lane < boxes, grouped = lane >= kGroups && lane < 2 * kGroups;
+    auto entry_of = [&](int step) {
+        const int key = step * kKeys + my_key;
+        return (boxed || grouped) && key < t.keys ? __ldg(table + (key >> a.page_shift)) : 0;
+    };
+    int entry = entry_of(0), sent_k = 0, sent_v = 0;
+    for (int j = 0; j < t.steps; ++j) {
+        const int key = j * kKeys + my_key;
+        const bool used = (boxed || grouped) && key < t.keys;
+        const int64_t page = used ? kv_page_ok(entry, a.num_pages) : -1;
+        const int z = page < 0 ? -1 : int(page) * a.kv_heads + t.head;
+        float ks = 0.f, vs = 0.f;
+        if (grouped && z >= 0) {
+            ks = __ldg(a.k_scale + z);
+            vs = __ldg(a.v_scale + z);
+        }
+        if (j + 1 < t.steps) entry = entry_of(j + 1);
+        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, boxed && z >= 0))) * uint32_t(box_rows) * 128u;
+        const int y = key & ((1 << a.page_shift) - 1);
+        if (j && !wait_warp(&bar.raw_k_free, (j - 1) & 1, abort)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar.raw_k_full, bytes);
+        __syncwarp();
+        if (boxed && z >= 0) tma_load_3d(kraw + lane * box_rows * 128, km, 0, y, z, &bar.raw_k_full);
+        sent_k = j + 1;
+        if (j && !wait_warp(&bar.raw_v_free, (j - 1) & 1, abort)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar.raw_v_full, bytes);
+        __syncwarp();
+        if (boxed && z >= 0) tma_load_3d(vraw + lane * box_rows * 128, vm, 0, y, z, &bar.raw_v_full);
+        sent_v = j + 1;
+        // ---- scales
+        const int set = j % kRing, g = lane - kGroups;
+        const bool bad = grouped && used && z < 0;
+        const uint32_t dead = __ballot_sync(0xffffffffu, bad) >> kGroups;
+        const bool normal = vs >= 0x1p-126f && vs <= 0x1p126f;
+        // (groups behind the last key: masked by their keys, any scale will do)
+        const bool plain = __all_sync(0xffffffffu, !grouped || !used || normal) && !dead;
+        const float top = __uint_as_float(warp_umax(__float_as_uint(fabsf(vs))));
+        if (grouped) {
+            sc.k[set][g] = ks * fabsf(a.sm_scale) * kLog2e;
+            sc.v[set][g] = vs;
+            sc.log_v[set][g] = log2_approx(vs);
+            sc.inv_v[set][g] = 1.f / vs;
+        }
+        if (lane == 0) {
+            sc.dead[set] = dead;
+            sc.plain[set] = plain;
+            sc.v_max[set] = top;
+            if (dead) atomicCAS(&g_kv_tiles_error, kErrNone, kErrRange);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sc_full[set]);
+    }
+    // nothing may land in shared memory after the block exits
+    if (sent_k) wait_warp(&bar.raw_k_full, (sent_k - 1) & 1, abort);
+    if (sent_v) wait_warp(&bar.raw_v_full, (sent_v - 1) & 1, abort);
+}
+
 // ------------------------------------------------------------------ codes to binary16
 template <bool F8, int DT>
-__device__ void convert_role(const KvAttnArgs &a, const Item &t, uint8_t *ksm, uint8_t *vsm, Scales &sc, Bars &bar,
-                             volatile int *abort)
+__device__ void convert_role(const KvAttnArgs &a, const Item &t, const uint8_t *kraw, const uint8_t *vraw, uint8_t *ksm,
+                             uint8_t *vsm, const Scales &sc, Bars &bar, volatile int *abort)
 {
     constexpr int kPerRow = DT / 16;                  // 16-byte chunks of a key
     constexpr int kPass = kConvThreads / kPerRow;     // keys of a pass
-    constexpr int kKp = kKeys / kPass;                // passes: 4 (DT 128) or 2
-    constexpr int kVt = DT / 64;                      // value tasks (8 keys x 4 dimensions) of a thread
+    constexpr int kKp = kKeys / kPass;                // passes: 8 (DT 128) or 4
+    constexpr int kVt = DT / 8 / kConvWarps;          // value tasks (8 keys x 4 dimensions) of a thread
     const int ct = threadIdx.x - 32 * kSoftWarps, cw = ct / 32, lane = ct % 32;
-    const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
-    const int last_page = (t.keys - 1) >> a.page_shift, slot_mask = (1 << a.page_shift) - 1;
     const int chunk = ct % kPerRow, krow = ct / kPerRow;
-    // values: a warp takes 32 keys x 32 dimensions; lanes so that both the 32-byte reads and the
-    // transposed 16-byte stores are free of conflicts
-    const int tg = lane % 8 / 2, dg = 2 * (lane / 8) + lane % 2;
-    auto entry_of = [&](int key) { return __ldg(table + min(key >> a.page_shift, last_page)); };
-    auto row_of = [&](int entry, int key) {
-        const int64_t page = kv_page_ok(entry, a.num_pages);
-        return kv_code_offset(page < 0 ? 0 : page, t.head, key & slot_mask, a.kv_heads, a.page_shift, a.pitch);
-    };
-    uint4 kraw[kKp];
-    uint32_t vraw[kVt][8];
-    int kent[kKp], vent[kVt], sent = 0;
-    float ks = 0.f, vs = 0.f;
-    bool sbad = false;
-    auto v_key = [&](int i) { return 32 * ((cw + 8 * i) % 4) + 8 * tg; };
-    auto v_dim = [&](int i) { return 32 * ((cw + 8 * i) / 4) + 4 * dg; };
-    auto load_entries = [&](int key0) {
-#pragma unroll
-        for (int i = 0; i < kKp; ++i) kent[i] = entry_of(key0 + krow + kPass * i);
-#pragma unroll
-        for (int i = 0; i < kVt; ++i) vent[i] = entry_of(key0 + v_key(i));
-        if (ct < kGroups) sent = entry_of(key0 + 16 * ct);
-    };
-    auto load_k = [&](int key0) {
-#pragma unroll
-        for (int i = 0; i < kKp; ++i)
-            kraw[i] = 16 * chunk < a.pitch ? ldg128(a.k + row_of(kent[i], key0 + krow + kPass * i) + 16 * chunk)
-                                           : make_uint4(0, 0, 0, 0);
-        if (ct < kGroups) {
-            const int64_t page = kv_page_ok(sent, a.num_pages);
-            sbad = page < 0 && key0 + 16 * ct < t.keys;
-            const int64_t si = kv_scale_index(page < 0 ? 0 : page, t.head, a.kv_heads);
-            ks = __ldg(a.k_scale + si);
-            vs = page < 0 ? 0.f : __ldg(a.v_scale + si);
-        }
-    };
-    auto load_v = [&](int key0) {
-#pragma unroll
-        for (int i = 0; i < kVt; ++i) {
-            const int key = key0 + v_key(i), d = v_dim(i);
-            const uint8_t *p = a.v + row_of(vent[i], key) + d;
-            const bool bad = kv_page_ok(vent[i], a.num_pages) < 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // slots behind the last key hold anything, e4m3 NaN codes among it
-                const bool dead = F8 && (bad || key + e >= t.keys);
-                vraw[i][e] = d < a.pitch && !dead ? ldg32(p + e * a.pitch) : 0u;
-            }
-        }
-    };
-    load_entries(0);
-    load_k(0);
-    load_v(0);
-    if (t.steps > 1) load_entries(kKeys);
+    // values: a warp takes 32 keys; its lanes 8 keys x 4 dimensions each, so that the transposed
+    // 16-byte stores are free of conflicts
+    const int tg = lane % 8 / 2, dg = 2 * (lane / 8) + lane % 2, vkey = 32 * cw + 8 * tg;
     for (int j = 0; j < t.steps; ++j) {
         const int buf = j & 1;
-        const bool more = j + 1 < t.steps;
         uint8_t *kb = ksm + buf * Layout<DT>::kQ, *vb = vsm + buf * Layout<DT>::kV;
         // ---- keys
+        if (!wait_warp(&bar.raw_k_full, j & 1, abort)) return;
         if (j >= 2 && !wait_warp(&bar.k_free[buf], ((j >> 1) - 1) & 1, abort)) return;
 #pragma unroll
         for (int i = 0; i < kKp; ++i) {
             const int r = krow + kPass * i;
-            uint32_t w[4] = {kraw[i].x, kraw[i].y, kraw[i].z, kraw[i].w};
-            if constexpr (F8) {
-                if (a.head_dim < a.pitch)  // bytes behind the head hold anything
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (16 * chunk + 4 * x >= a.head_dim) w[x] = 0u;
-            } else {
+            const uint4 raw = lds128(kraw + r * 128 + ((chunk ^ (r & 7)) << 4));
+            uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+            if constexpr (!F8) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) w[x] ^= 0x80808080u;
             }
@@ -208,33 +251,36 @@ __device__ void convert_role(const KvAttnArgs &a, const Item &t, uint8_t *ksm, u
             sts128(row + (((c + swap) ^ (r & 7)) << 4), swap ? hi : lo);
             sts128(row + (((c + !swap) ^ (r & 7)) << 4), swap ? lo : hi);
         }
-        if (cw == 0) {
-            const uint32_t dead = __ballot_sync(0xffffffffu, sbad) & ((1u << kGroups) - 1);
-            if (lane < kGroups) {
-                sc.k[j % kRing][lane] = ks * a.sm_scale * kLog2e;
-                sc.v[j % kRing][lane] = vs;
-            }
-            if (lane == 0) {
-                sc.dead[j % kRing] = dead;
-                if (dead) atomicCAS(&g_kv_tiles_error, kErrNone, kErrRange);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.sc_full[j % kRing]);
-        }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_full[buf]);
-        if (more) load_k((j + 1) * kKeys);
+        if (lane == 0) {
+            mbar_arrive(&bar.raw_k_free);
+            mbar_arrive(&bar.k_full[buf]);
+        }
         // ---- values
+        if (!wait_warp(&bar.raw_v_full, j & 1, abort)) return;
         if (j >= 2 && !wait_warp(&bar.v_free[buf], ((j >> 1) - 1) & 1, abort)) return;
+        int left = t.keys - j * kKeys - vkey;  // keys of the lane's eight that hold codes
+        // a page that is none was not copied (its weights are 0, but e4m3 may hold NaN codes)
+        if (F8 && wait_warp(&bar.sc_full[j % kRing], (j / kRing) & 1, abort) && (sc.dead[j % kRing] >> (vkey / 16) & 1)) left = 0;
 #pragma unroll
         for (int i = 0; i < kVt; ++i) {
-            const int key = v_key(i), d = v_dim(i);
+            const int d = 32 * i + 4 * dg;
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = lds32(vraw + (vkey + e) * 128 + (((d >> 4) ^ e) << 4) + (d & 15));
+            if (F8 && left < 8) {
+                // slots behind the last key hold anything, e4m3 NaN codes among it
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= left) w[e] = 0u;
+            }
             uint32_t o[4][4];  // [dimension][pair of keys]
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                uint32_t x = prmt(vraw[i][2 * e], vraw[i][2 * e + 1], 0x5140);
-                uint32_t y = prmt(vraw[i][2 * e], vraw[i][2 * e + 1], 0x7362);
+                uint32_t x = prmt(w[2 * e], w[2 * e + 1], 0x5140);
+                uint32_t y = prmt(w[2 * e], w[2 * e + 1], 0x7362);
                 if constexpr (!F8) {
                     x ^= 0x80808080u;
                     y ^= 0x80808080u;
@@ -244,19 +290,18 @@ __device__ void convert_role(const KvAttnArgs &a, const Item &t, uint8_t *ksm, u
                 o[2][e] = widen<F8, 0>(y);
                 o[3][e] = widen<F8, 1>(y);
             }
-            if (d < a.pitch) {
-                uint8_t *base = vb + key / 64 * (DT * 128);
-                const int c = key % 64 / 8;
+            uint8_t *base = vb + vkey / 64 * (DT * 128);
+            const int c = vkey % 64 / 8;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    sts128(base + (d + x) * 128 + ((c ^ ((d + x) & 7)) << 4), make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]));
-            }
+            for (int x = 0; x < 4; ++x)
+                sts128(base + (d + x) * 128 + ((c ^ ((d + x) & 7)) << 4), make_uint4(o[x][0], o[x][1], o[x][2], o[x][3]));
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_full[buf]);
-        if (more) load_v((j + 1) * kKeys);
-        if (j + 2 < t.steps) load_entries((j + 2) * kKeys);
+        if (lane == 0) {
+            mbar_arrive(&bar.raw_v_free);
+            mbar_arrive(&bar.v_full[buf]);
+        }
     }
 }
 
@@ -331,7 +376,8 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
     const uint32_t tlane = tbase + (uint32_t(32 * (warp % 4)) << 16);
     const uint32_t scol = tlane + kScol + 128 * tile, ocol = tlane + kOcol + 128 * tile;
 
-    // ---- the query row, binary16 (bfloat16 rows scaled by a power of two, see load_queries)
+    // ---- the query row with sm_scale's sign, binary16 (bfloat16 rows scaled by a power of two so that
+    // the largest value fits: what is lost below is under 2^-25 of it)
     float unscale = 1.f;
     {
         const uint16_t *q = static_cast<const uint16_t *>(a.q) + at;
@@ -344,7 +390,7 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y))));
             }
             const int e = kv_clamp(int(__float_as_uint(amax) >> 23) - 127, -120, 120);
-            up = __uint_as_float(uint32_t(127 - e) << 23);
+            up = copysignf(__uint_as_float(uint32_t(127 - e) << 23), a.sm_scale);
             unscale = __uint_as_float(uint32_t(127 + e) << 23);
         }
         uint8_t *base = qsm + tile * Layout<DT>::kQ + r * 128;
@@ -357,6 +403,9 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
                 if constexpr (BF16) {
                     const float2 lo = act_f2<T>(x[k].x), hi = act_f2<T>(x[k].y);
                     x[k] = make_uint2(act_t2<__half>(lo.x * up, lo.y * up), act_t2<__half>(hi.x * up, hi.y * up));
+                } else if (a.sm_scale < 0.f) {
+                    x[k].x ^= 0x80008000u;
+                    x[k].y ^= 0x80008000u;
                 }
             }
             sts128(base + c / 8 * Layout<DT>::kAtom + (((c % 8) ^ (r & 7)) << 4), make_uint4(x[0].x, x[0].y, x[1].x, x[1].y));
@@ -371,34 +420,40 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
         const int set = j % kRing, key0 = j * kKeys;
         if (!wait_warp(&bar.sc_full[set], (j / kRing) & 1, abort) || !wait_warp(&bar.s_full[tile], j & 1, abort)) return;
         tc::fence_after_sync();
-        const uint32_t dead = sc.dead[set];
         const int left = seen - key0;  // keys of this step that the row sees
-        const bool masked = __any_sync(0xffffffffu, left < kKeys) || dead;
-        float kc[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) kc[g] = sc.k[set][g] * unscale;
-        // ---- maximum
+        const bool plain = __all_sync(0xffffffffu, left >= kKeys) && sc.plain[set];
+        const uint32_t dead = sc.dead[set];
+        // ---- maximum (loops over chunks of 32 keys stay loops: unrolled, the roles' code would not
+        // fit the instruction cache)
         float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             uint32_t s[32];
             tc::ld_32x32b_x32(scol + 32 * c, s);
             tc::wait_ld();
-            if (masked) {
+            if (!plain) {
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
-                    if (32 * c + x < left && !(dead >> (2 * c + x / 16) & 1))
-                        mx = fmaxf(mx, __uint_as_float(s[x]) * kc[2 * c + x / 16]);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(s[x]) * kc[2 * c + x / 16]);
+                    if (32 * c + x >= left || (dead >> (2 * c + x / 16) & 1)) s[x] = 0xff800000u;  // -inf
             }
+            float top[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float y[4];  // (scales are not negative: the largest product is the largest score's)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    y[x] = fmaxf(__uint_as_float(s[16 * h + x]), __uint_as_float(s[16 * h + 4 + x]));
+                    y[x] = fmaxf(fmaxf(y[x], __uint_as_float(s[16 * h + 8 + x])), __uint_as_float(s[16 * h + 12 + x]));
+                }
+                top[h] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            }
+            // -inf stays -inf where a scale is 0
+            mx = fmaxf(mx, top[0] == -INFINITY ? top[0] : top[0] * (sc.k[set][2 * c] * unscale));
+            mx = fmaxf(mx, top[1] == -INFINITY ? top[1] : top[1] * (sc.k[set][2 * c + 1] * unscale));
         }
         const float m_new = mx > m + kSlack ? mx : m;  // -inf until the row sees a key
         // ---- reference of the value scales: a power of two above all so far
-        float vmax = 0.f;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) vmax = fmaxf(vmax, fabsf(sc.v[set][g]));
+        const float vmax = sc.v_max[set];
         const float vnew = vmax >= vref && vmax > 0.f
                                ? __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u) : vref;
         const float inv = vnew > 0.f ? 1.f / vnew : 0.f;
@@ -408,7 +463,7 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
         if (j > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
             if (!wait_warp(&bar.o_done[tile], (j - 1) & 1, abort)) return;
             tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DT / 32; ++c) {
                 uint32_t o[32];
                 tc::ld_32x32b_x32(ocol + 32 * c, o);
@@ -423,26 +478,58 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
         vref = vnew;
         // ---- weights, over the scores that are already read
         const float base = m == -INFINITY ? 0.f : m - kRaise;
+        if (plain) {
+            // the value scale as part of the exponent: P = 2^(x - base + log2(vs / vref)); the weight
+            // sum takes the group's sum back over vs / vref
+            const float log_ref = float(int(__float_as_uint(vref) >> 23) - 127);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t s[32], p[16];
+                tc::ld_32x32b_x32(scol + 32 * c, s);
+                tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t s[32], p[16];
-            tc::ld_32x32b_x32(scol + 32 * c, s);
-            tc::wait_ld();
+                for (int h = 0; h < 2; ++h) {
+                    const int g = 2 * c + h;
+                    const float k = sc.k[set][g] * unscale, off = sc.log_v[set][g] - log_ref - base;
+                    const float2 k2 = make_float2(k, k), off2 = make_float2(off, off);
+                    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                const int g = 2 * c + x / 16;
-                float w0 = exp2_approx(fmaf(__uint_as_float(s[x]), kc[g], -base));
-                float w1 = exp2_approx(fmaf(__uint_as_float(s[x + 1]), kc[g], -base));
-                if (masked) {
-                    const bool gd = dead >> g & 1;
-                    if (32 * c + x >= left || gd) w0 = 0.f;
-                    if (32 * c + x + 1 >= left || gd) w1 = 0.f;
+                    for (int x = 0; x < 16; x += 2) {
+                        const float2 e = fma2(make_float2(__uint_as_float(s[16 * h + x]), __uint_as_float(s[16 * h + x + 1])), k2, off2);
+                        const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                        sum = add2(sum, w);
+                        p[8 * h + x / 2] = act_t2<__half>(w.x, w.y);
+                    }
+                    l = fmaf(sum.x + sum.y, vref * sc.inv_v[set][g], l);
                 }
-                l += w0 + w1;
-                const float v = sc.v[set][g] * inv;
-                p[x / 2] = act_t2<__half>(w0 * v, w1 * v);
+                tc::st_32x32b_x16(scol + 16 * c, p);
             }
-            tc::st_32x32b_x16(scol + 16 * c, p);
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t s[32], p[16];
+                tc::ld_32x32b_x32(scol + 32 * c, s);
+                tc::wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int g = 2 * c + h;
+                    const float k = sc.k[set][g] * unscale, v = sc.v[set][g] * inv;
+                    const bool gone = dead >> g & 1;
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        float w[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = 16 * h + x + e;
+                            w[e] = exp2_approx(fmaf(__uint_as_float(s[at]), k, -base));
+                            if (32 * c + at >= left || gone) w[e] = 0.f;
+                        }
+                        l += w[0] + w[1];
+                        p[8 * h + x / 2] = act_t2<__half>(w[0] * v, w[1] * v);
+                    }
+                }
+                tc::st_32x32b_x16(scol + 16 * c, p);
+            }
         }
         tc::wait_st();
         tc::fence_before_sync();
@@ -472,7 +559,9 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
 }
 
 template <bool F8, bool BF16, int DT>
-__global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles_kernel(const __grid_constant__ KvAttnArgs a)
+__global__ void __launch_bounds__(kThreads, 1)
+kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                     const __grid_constant__ KvAttnArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Bars bar;
@@ -481,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles_kernel(const __grid
     __shared__ int abort_flag, s_seq[4];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qsm = smem, *ksm = qsm + 2 * Layout<DT>::kQ, *vsm = ksm + 2 * Layout<DT>::kQ;
+    uint8_t *kraw = vsm + 2 * Layout<DT>::kV, *vraw = kraw + Layout<DT>::kRaw;
     volatile int *abort = &abort_flag;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     grid_dep_launch();
@@ -531,10 +621,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles_kernel(const __grid
             mbar_init(&bar.o_done[i], 1);
         }
         for (int i = 0; i < kRing; ++i) mbar_init(&bar.sc_full[i], 1);
+        mbar_init(&bar.raw_k_full, 1);
+        mbar_init(&bar.raw_v_full, 1);
+        mbar_init(&bar.raw_k_free, kConvWarps);
+        mbar_init(&bar.raw_v_free, kConvWarps);
         mbar_init(&bar.fin, 1);
         fence_barrier_init();
+        tma_prefetch_desc(&km);
+        tma_prefetch_desc(&vm);
     }
-    if (warp == kSoftWarps + kConvWarps) {
+    if (warp == kMmaWarp) {
         tc::tmem_alloc(&tmem_slot, kTmemCols);
         tc::tmem_relinquish();
     }
@@ -546,8 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles_kernel(const __grid
     if (warp < kSoftWarps) {
         softmax_role<BF16, DT>(a, t, qsm, sc, bar, tbase, abort);
     } else if (t.steps > 0) {
-        if (warp < kSoftWarps + kConvWarps)
-            convert_role<F8, DT>(a, t, ksm, vsm, sc, bar, abort);
+        if (warp < kMmaWarp)
+            convert_role<F8, DT>(a, t, kraw, vraw, ksm, vsm, sc, bar, abort);
+        else if (warp == kCopyWarp)
+            copy_role(a, t, &km, &vm, kraw, vraw, sc, bar, abort);
         else if (lane == 0)
             mma_role<DT>(a, t, smem_u32(qsm), smem_u32(ksm), smem_u32(vsm), bar, tbase, abort);
     }
@@ -555,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles_kernel(const __grid
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kSoftWarps + kConvWarps) tc::tmem_dealloc(tbase, kTmemCols);
+    if (warp == kMmaWarp) tc::tmem_dealloc(tbase, kTmemCols);
 }
 
 template <bool F8, bool BF16>
@@ -578,8 +676,11 @@ wq_status kv_attn_tiles(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st
         return check_launch("cudaFuncSetAttribute(kv_attn_tiles_kernel)");
     const int64_t blocks = kv_row_item(a.M, a.n_seqs, a.group, kRows) * a.kv_heads;
     if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
+    CUtensorMap km, vm;
+    wq_status rc = encode_cache(&km, &vm, a, 128, std::min(1 << a.page_shift, kKeys));
+    if (rc != WQ_OK) return rc;
     PreparedLaunch L;
-    L.set(fn, dim3(unsigned(blocks)), dim3(kThreads), size_t(smem), a);
+    set_attn_launch(L, fn, unsigned(blocks), kThreads, size_t(smem), km, vm, a);
     return launch_prepared(L, st, "kv_attn_tiles_kernel");
 }
 

@@ -270,7 +270,7 @@ wq_status rmsnorm_quant_fp8(const void *X, const void *residual, const void *gam
  *   k, v              [num_pages, kv_heads, page_size, pitch] bytes, pitch = head_dim rounded up
  *                     to a multiple of 16 (bytes head_dim .. pitch - 1 are neither written nor
  *                     used)
- *   k_scale, v_scale  [num_pages, kv_heads] binary32
+ *   k_scale, v_scale  [num_pages, kv_heads] binary32, finite and not negative
  * page_size 16, 32, 64, 128 or 256; head_dim a multiple of 4 from 16 to 256; kv_heads 1 to 1024;
  * format WQ_FMT_INT (INT8) or WQ_FMT_E4M3.  k and v 16-byte aligned.  Nothing needs to be
  * cleared before first use. */
