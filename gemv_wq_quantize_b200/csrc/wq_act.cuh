@@ -28,11 +28,22 @@ __device__ __forceinline__ float2 act_f2(uint32_t w)
     return make_float2(act_f(e[0]), act_f(e[1]));
 }
 template <typename T>
-__device__ __forceinline__ uint32_t act_t2(float a, float b)
+__device__ __forceinline__ uint32_t act_t2(float a, float b);
+// (one packed conversion: two single ones would go through the slow conversion pipe)
+template <>
+__device__ __forceinline__ uint32_t act_t2<__half>(float a, float b)
 {
-    const T e[2] = {act_t<T>(a), act_t<T>(b)};
+    const __half2 v = __floats2half2_rn(a, b);
     uint32_t w;
-    memcpy(&w, e, 4);
+    memcpy(&w, &v, 4);
+    return w;
+}
+template <>
+__device__ __forceinline__ uint32_t act_t2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    uint32_t w;
+    memcpy(&w, &v, 4);
     return w;
 }
 

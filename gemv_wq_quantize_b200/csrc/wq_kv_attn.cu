@@ -685,9 +685,7 @@ __device__ __forceinline__ int share_of(int total, int c, int grid)
 }
 
 template <bool F8, bool BF16, int DT, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<DT, NT>::kPerSm)
-kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
-                    const __grid_constant__ KvAttnArgs a)
+__device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtensorMap &vm, const KvAttnArgs &a)
 {
     using S = Shape<DT, NT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -703,7 +701,7 @@ kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constan
         tma_prefetch_desc(&vm);
     }
     grid_dep_launch();
-    grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
+    if (!a.behind_tiles) grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
 
     // units of every sequence, summed up: each thread takes a run of sequences
     const bool split = a.partials != nullptr;
@@ -822,6 +820,15 @@ kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constan
     for (int i = 0; i < 2; ++i)
         if (kept_any[i] && sm.parts[i])
             join_parts<T, DT, NT>(a, kept[i], a.partials + int64_t(sm.first[i]) * (2 * kSlot), sm.parts[i]);
+}
+
+template <bool F8, bool BF16, int DT, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<DT, NT>::kPerSm)
+kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                    const __grid_constant__ KvAttnArgs a)
+{
+    attend_rows<F8, BF16, DT, NT>(km, vm, a);
+    if (a.behind_tiles) grid_dep_wait();
 }
 
 struct RowsPlan {
@@ -958,6 +965,10 @@ extern "C" wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t
     const bool bf16 = dt == WQ_BF16, f8 = cache->format == WQ_FMT_E4M3;
     const bool tiles = a.head_dim <= 128 && M * a.group > kFewRows * batch->n_seqs;
     a.few_rows = tiles ? kFewRows : 0x7fffffff;
-    rc = kv_attn_rows(a, bf16, f8, stream);
-    return rc == WQ_OK && tiles ? kv_attn_tiles(a, bf16, f8, stream) : rc;
+    if (tiles) {
+        rc = kv_attn_tiles(a, bf16, f8, stream);
+        if (rc != WQ_OK) return rc;
+        a.behind_tiles = true;
+    }
+    return kv_attn_rows(a, bf16, f8, stream);
 }

@@ -19,6 +19,11 @@ struct KvAttnArgs {
     int page_shift, pitch, capacity;
     float sm_scale;
     int few_rows;         // sequences with more rows per key head go to the tile kernel
+    // The kernel for few rows, launched behind the tile kernel of the same call, runs beside it: every
+    // block of the tile kernel has waited for the kernels before when it lets the next grid start,
+    // so the one started needs no wait of its own for them.  It waits for the tile kernel's end at
+    // its own end, so that what follows has both behind it.
+    bool behind_tiles;
     float *partials;      // nullptr: every tile is walked by one block
     unsigned *arrivals;
 };

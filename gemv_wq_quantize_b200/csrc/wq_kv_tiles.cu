@@ -10,10 +10,9 @@
 // about as much; so the two 128-row tiles of a block take turns: while one tile's products run,
 // the other tile's softmax does.
 //  * warps 0-3 / 4-7: tile 0 / 1, a thread per row: query row to shared memory, then per key
-//    block: scores from Tensor Memory (twice: maximum, then weights), weights back over them as
+//    block: scores from Tensor Memory, weights back over them as
 //    the A operand of the second product.  O stays in Tensor Memory; it is rescaled only when the
-//    maximum rose by more than 2^kSlack or a larger value scale arrived, which is rare after the
-//    first blocks.
+//    maximum rose too far or a larger value scale arrived, which is rare after the first blocks.
 //  * warps 8-11: codes widened to binary16 into the 128-byte swizzled layout of the MMA's K-major
 //    operands: keys as rows of dimensions, values transposed as rows of keys.
 //  * warp 12: one thread issues the MMAs.
@@ -81,9 +80,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 constexpr int kRing = 4;             // scale sets: a set is rewritten once both tiles are two steps on
 constexpr uint32_t kTmemCols = 512, kScol = 0, kOcol = 256;  // two 128-column tiles of each
 
-// A maximum that rises by less than 2^kSlack is not followed, so weights reach 2^kSlack; raised
-// by 2^kRaise they reach 2^15 in binary16, and are exact to half a step down to 2^-(14 + kRaise).
-constexpr float kSlack = 4.f, kRaise = 11.f;
+// Weights are raised by 2^kRaise: exact to half a step down to 2^-(14 + kRaise) in binary16.  A
+// maximum that rises a little is not followed while all weights fit: 2^kRaise times the rise.
+constexpr float kRaise = 11.f;
 
 struct Bars {
     uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], sc_full[kRing];
@@ -141,7 +140,8 @@ struct Item {
     KvSpan s;
     int b, head, row0, rows;  // the block's rows
     int keys;                 // keys that its last row sees
-    int steps, tiles;
+    int steps, tiles;         // key steps of the block (of its last tile)
+    int steps_of[2];          // of each tile: the first sees fewer keys
 };
 
 // ------------------------------------------------------------------ codes to shared memory
@@ -195,8 +195,8 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, co
         if (grouped) {
             sc.k[set][g] = ks * fabsf(a.sm_scale) * kLog2e;
             sc.v[set][g] = vs;
-            sc.log_v[set][g] = log2_approx(vs);
-            sc.inv_v[set][g] = 1.f / vs;
+            sc.log_v[set][g] = used ? log2_approx(vs) : 0.f;  // (all keys of an unused group are masked)
+            sc.inv_v[set][g] = used ? 1.f / vs : 0.f;
         }
         if (lane == 0) {
             sc.dead[set] = dead;
@@ -214,7 +214,7 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, co
 
 // ------------------------------------------------------------------ codes to binary16
 template <bool F8, int DT>
-__device__ void convert_role(const KvAttnArgs &a, const Item &t, const uint8_t *kraw, const uint8_t *vraw, uint8_t *ksm,
+__device__ __noinline__ void convert_role(const KvAttnArgs &a, const Item &t, const uint8_t *kraw, const uint8_t *vraw, uint8_t *ksm,
                              uint8_t *vsm, const Scales &sc, Bars &bar, volatile int *abort)
 {
     constexpr int kPerRow = DT / 16;                  // 16-byte chunks of a key
@@ -232,7 +232,7 @@ __device__ void convert_role(const KvAttnArgs &a, const Item &t, const uint8_t *
         // ---- keys
         if (!wait_warp(&bar.raw_k_full, j & 1, abort)) return;
         if (j >= 2 && !wait_warp(&bar.k_free[buf], ((j >> 1) - 1) & 1, abort)) return;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kKp; ++i) {
             const int r = krow + kPass * i;
             const uint4 raw = lds128(kraw + r * 128 + ((chunk ^ (r & 7)) << 4));
@@ -263,7 +263,7 @@ __device__ void convert_role(const KvAttnArgs &a, const Item &t, const uint8_t *
         int left = t.keys - j * kKeys - vkey;  // keys of the lane's eight that hold codes
         // a page that is none was not copied (its weights are 0, but e4m3 may hold NaN codes)
         if (F8 && wait_warp(&bar.sc_full[j % kRing], (j / kRing) & 1, abort) && (sc.dead[j % kRing] >> (vkey / 16) & 1)) left = 0;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kVt; ++i) {
             const int d = 32 * i + 4 * dg;
             uint32_t w[8];
@@ -310,43 +310,51 @@ template <int DT>
 __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uint32_t kaddr, uint32_t vaddr, Bars &bar,
                          uint32_t tbase, volatile int *abort)
 {
-    const uint32_t iqk = tc::idesc_f16(false, kTile, kKeys), ipv = tc::idesc_f16(false, kTile, a.pitch);
+    const uint32_t iqk = tc::idesc_f16(false, kTile, kKeys), ipv = tc::idesc_f16(false, kTile, DT);
+    // descriptors differ in their address field only: the offsets below are constants added to the
+    // low word
     const uint64_t dq = tc::sdesc_sw128(qaddr), dk = tc::sdesc_sw128(kaddr), dv = tc::sdesc_sw128(vaddr);
-    const int ksteps = a.pitch / 16;
+    const uint32_t high = uint32_t(dq >> 32), q_lo = uint32_t(dq), k_lo = uint32_t(dk), v_lo = uint32_t(dv);
+    auto desc = [&](uint32_t lo) { return uint64_t(high) << 32 | lo; };
     auto qk = [&](int tile, int buf) {
-        const uint64_t q = dq + uint64_t(tile * Layout<DT>::kQ >> 4), k = dk + uint64_t(buf * Layout<DT>::kQ >> 4);
-        for (int i = 0; i < ksteps; ++i) {
-            const uint64_t off = uint64_t(((i >> 2) * Layout<DT>::kAtom + (i & 3) * 32) >> 4);
-            tc::mma_f16_ss(tbase + kScol + 128 * tile, q + off, k + off, iqk, i > 0);
+        const uint32_t q = q_lo + uint32_t(tile * Layout<DT>::kQ >> 4), k = k_lo + uint32_t(buf * Layout<DT>::kQ >> 4);
+#pragma unroll
+        for (int i = 0; i < DT / 16; ++i) {
+            const uint32_t off = uint32_t(((i >> 2) * Layout<DT>::kAtom + (i & 3) * 32) >> 4);
+            tc::mma_f16_ss(tbase + kScol + 128 * tile, desc(q + off), desc(k + off), iqk, i > 0);
         }
         tc::commit(&bar.s_full[tile]);
     };
     auto pv = [&](int tile, int buf, bool first) {
-        const uint64_t v = dv + uint64_t(buf * Layout<DT>::kV >> 4);
+        const uint32_t v = v_lo + uint32_t(buf * Layout<DT>::kV >> 4);
 #pragma unroll
         for (int i = 0; i < kKeys / 16; ++i) {
-            const uint64_t off = uint64_t(((i >> 2) * (DT * 128) + (i & 3) * 32) >> 4);
-            tc::mma_f16_ts(tbase + kOcol + 128 * tile, tbase + kScol + 128 * tile + 8 * i, v + off, ipv, !first || i > 0);
+            const uint32_t off = uint32_t(((i >> 2) * (DT * 128) + (i & 3) * 32) >> 4);
+            tc::mma_f16_ts(tbase + kOcol + 128 * tile, tbase + kScol + 128 * tile + 8 * i, desc(v + off), ipv, !first || i > 0);
         }
         tc::commit(&bar.o_done[tile]);
     };
     if (!wait(&bar.q_full, 0, abort) || !wait(&bar.k_full[0], 0, abort)) return;
     tc::fence_after_sync();
-    for (int tile = 0; tile < t.tiles; ++tile) qk(tile, 0);
+    for (int tile = 0; tile < t.tiles; ++tile)
+        if (t.steps_of[tile]) qk(tile, 0);
     tc::commit(&bar.k_free[0]);
     bool ok = true;
     for (int j = 0; j < t.steps && ok; ++j) {
         const int buf = j & 1, nbuf = buf ^ 1;
-        const bool more = j + 1 < t.steps;
+        bool have_v = false, have_k = false;
         for (int tile = 0; tile < t.tiles; ++tile) {
-            ok = wait(&bar.p_full[tile], j & 1, abort) && (tile || wait(&bar.v_full[buf], (j >> 1) & 1, abort));
+            if (j >= t.steps_of[tile]) continue;
+            ok = wait(&bar.p_full[tile], j & 1, abort) && (have_v || wait(&bar.v_full[buf], (j >> 1) & 1, abort));
             if (!ok) break;
+            have_v = true;
             tc::fence_after_sync();
             pv(tile, buf, j == 0);
-            if (more) {
-                if (!tile) {
+            if (j + 1 < t.steps_of[tile]) {
+                if (!have_k) {
                     ok = wait(&bar.k_full[nbuf], ((j + 1) >> 1) & 1, abort);
                     if (!ok) break;
+                    have_k = true;
                     tc::fence_after_sync();
                 }
                 qk(tile, nbuf);  // behind the tile's second product in the pipe: it may overwrite the weights
@@ -354,13 +362,138 @@ __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uin
         }
         if (!ok) break;
         tc::commit(&bar.v_free[buf]);
-        if (more) tc::commit(&bar.k_free[nbuf]);
+        if (j + 1 < t.steps) tc::commit(&bar.k_free[nbuf]);
     }
     tc::commit(&bar.fin);  // all MMAs complete before the Tensor Memory is freed
     wait(&bar.fin, 0, abort);
 }
 
 // ------------------------------------------------------------------ softmax (a thread per row)
+// The weights of a step in one pass over its scores (see softmax_role), stored over them if all of
+// the warp fit binary16 (true; any: whatever they are), else nothing is.  MASKED: some row sees fewer
+// than all keys.
+template <bool MASKED>
+__device__ __forceinline__ bool weights_once(uint32_t scol, const float *ks, const float *log_v, const float *inv_v,
+                                             float unscale, float shift, int left, float &lsum, bool any)
+{
+    uint32_t p[4][16], s[2][16];
+    float most = 0.f;
+    tc::ld_32x32b_x16(scol, s[0]);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        tc::wait_ld();
+        if (g + 1 < kGroups) tc::ld_32x32b_x16(scol + 16 * (g + 1), s[(g + 1) & 1]);
+        if (MASKED)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (16 * g + i >= left) s[g & 1][i] = 0xff800000u;  // -inf: weight 0
+        // (a scale of 0 times -inf would be NaN)
+        const float k = MASKED ? fmaxf(ks[g] * unscale, 0x1p-126f) : ks[g] * unscale, off = log_v[g] + shift;
+        const float2 k2 = make_float2(k, k), off2 = make_float2(off, off);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float2 e = fma2(make_float2(__uint_as_float(s[g & 1][i]), __uint_as_float(s[g & 1][i + 1])), k2, off2);
+            const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            sum = add2(sum, w);
+            p[g / 2][8 * (g % 2) + i / 2] = act_t2<__half>(w.x, w.y);
+        }
+        const float both = sum.x + sum.y;
+        most = both <= 61440.f ? most : INFINITY;  // (NaN too)
+        lsum = fmaf(both, inv_v[g], lsum);
+    }
+    if (!__all_sync(0xffffffffu, most == 0.f || any)) return false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tc::st_32x32b_x16(scol + 16 * c, p[c]);
+    tc::wait_st();
+    return true;
+}
+
+// The running references after a step: the maximum m over its scores too and, vref, a power of two
+// above its value scales, with l and the output tile taken over to them.  False: gave up.
+// (Loops over chunks of 32 keys stay loops: unrolled, the roles' code does not fit the instruction
+// cache, and blocks of few steps run it cold.)
+template <int DT>
+__device__ __forceinline__ bool new_references(uint32_t scol, uint32_t ocol, const Scales &sc, int set, float unscale,
+                                               int left, bool all, uint32_t dead, int j, int tile, Bars &bar,
+                                               volatile int *abort, float &m, float &vref, float &l)
+{
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+        tc::ld_32x32b_x32(scol + 32 * c, s);
+        tc::wait_ld();
+        if (!all) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                if (32 * c + x >= left || (dead >> (2 * c + x / 16) & 1)) s[x] = 0xff800000u;  // -inf
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float y[4];  // (scales are not negative: the largest product is the largest score's)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                y[x] = fmaxf(__uint_as_float(s[16 * h + x]), __uint_as_float(s[16 * h + 4 + x]));
+                y[x] = fmaxf(fmaxf(y[x], __uint_as_float(s[16 * h + 8 + x])), __uint_as_float(s[16 * h + 12 + x]));
+            }
+            const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            // -inf stays -inf where a scale is 0
+            mx = fmaxf(mx, top == -INFINITY ? top : top * (sc.k[set][2 * c + h] * unscale));
+        }
+    }
+    const float m_new = fmaxf(m, mx), vmax = sc.v_max[set];
+    const float vnew = vmax >= vref && vmax > 0.f ? __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u) : vref;
+    const float fm = m_new == m ? 1.f : exp2_approx(m - m_new);
+    const float fo = vnew == vref ? fm : fm * (vref * (1.f / vnew));
+    l *= fm;
+    m = m_new;
+    vref = vnew;
+    if (j > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
+        if (!wait_warp(&bar.o_done[tile], (j - 1) & 1, abort)) return false;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < DT / 32; ++c) {
+            uint32_t o[32];
+            tc::ld_32x32b_x32(ocol + 32 * c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
+            tc::st_32x32b_x32(ocol + 32 * c, o);
+        }
+        tc::wait_st();
+    }
+    return true;
+}
+
+// The weights of a step with groups that are no pages or value scales that have no logarithm.
+__device__ __forceinline__ void weights_any(uint32_t scol, const Scales &sc, int set, float unscale, int left, uint32_t dead,
+                                            float m, float vref, float &l)
+{
+    const float base = m == -INFINITY ? 0.f : m - kRaise, inv = vref > 0.f ? 1.f / vref : 0.f;
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g) {
+        uint32_t s[16], p[8];
+        tc::ld_32x32b_x16(scol + 16 * g, s);
+        tc::wait_ld();
+        const float k = sc.k[set][g] * unscale, v = sc.v[set][g] * inv;
+        const bool gone = dead >> g & 1;
+#pragma unroll
+        for (int x = 0; x < 16; x += 2) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[e] = exp2_approx(fmaf(__uint_as_float(s[x + e]), k, -base));
+                if (16 * g + x + e >= left || gone) w[e] = 0.f;
+            }
+            l += w[0] + w[1];
+            p[x / 2] = act_t2<__half>(w[0] * v, w[1] * v);
+        }
+        tc::st_32x32b_x8(scol + 8 * g, p);
+    }
+    tc::wait_st();
+}
+
 template <bool BF16, int DT>
 __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, const Scales &sc, Bars &bar,
                              uint32_t tbase, volatile int *abort)
@@ -376,185 +509,120 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
     const uint32_t tlane = tbase + (uint32_t(32 * (warp % 4)) << 16);
     const uint32_t scol = tlane + kScol + 128 * tile, ocol = tlane + kOcol + 128 * tile;
 
-    // ---- the query row with sm_scale's sign, binary16 (bfloat16 rows scaled by a power of two so that
-    // the largest value fits: what is lost below is under 2^-25 of it)
+    // ---- the warp's 32 query rows to shared memory, a row at a time across the lanes: with
+    // sm_scale's sign, binary16 (bfloat16 rows scaled by a power of two so that the largest value
+    // fits: what is lost below is under 2^-25 of it)
+    const int steps = t.steps_of[tile];
+    const uint32_t lives = __ballot_sync(0xffffffffu, live);
+    const int d4 = 4 * lane;  // the lane's four values of a row
+    uint8_t *rows_sm = qsm + tile * Layout<DT>::kQ + 32 * (warp % 4) * 128;
     float unscale = 1.f;
-    {
-        const uint16_t *q = static_cast<const uint16_t *>(a.q) + at;
-        float up = 1.f;
-        if constexpr (BF16) {
-            float amax = 0.f;
-            for (int d = 0; d < a.head_dim && live; d += 4) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(q + d);
-                const float2 lo = act_f2<T>(x.x), hi = act_f2<T>(x.y);
-                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y))));
-            }
-            const int e = kv_clamp(int(__float_as_uint(amax) >> 23) - 127, -120, 120);
-            up = copysignf(__uint_as_float(uint32_t(127 - e) << 23), a.sm_scale);
-            unscale = __uint_as_float(uint32_t(127 + e) << 23);
-        }
-        uint8_t *base = qsm + tile * Layout<DT>::kQ + r * 128;
-        for (int c = 0; c < DT / 8; ++c) {
-            uint2 x[2];
+    constexpr int kBatch = 8;  // rows whose loads are in flight together
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += kBatch) {
+        uint2 x[kBatch];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int d = 8 * c + 4 * k;
-                x[k] = live && d < a.head_dim ? *reinterpret_cast<const uint2 *>(q + d) : make_uint2(0, 0);
-                if constexpr (BF16) {
-                    const float2 lo = act_f2<T>(x[k].x), hi = act_f2<T>(x[k].y);
-                    x[k] = make_uint2(act_t2<__half>(lo.x * up, lo.y * up), act_t2<__half>(hi.x * up, hi.y * up));
-                } else if (a.sm_scale < 0.f) {
-                    x[k].x ^= 0x80008000u;
-                    x[k].y ^= 0x80008000u;
-                }
-            }
-            sts128(base + c / 8 * Layout<DT>::kAtom + (((c % 8) ^ (r & 7)) << 4), make_uint4(x[0].x, x[0].y, x[1].x, x[1].y));
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t from = __shfl_sync(0xffffffffu, at, r0 + k);
+            x[k] = (lives >> (r0 + k) & 1) && d4 < a.head_dim
+                       ? *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + from + d4) : make_uint2(0, 0);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.q_full);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if constexpr (BF16) {
+                const float2 lo = act_f2<T>(x[k].x), hi = act_f2<T>(x[k].y);
+                const float amax = __uint_as_float(warp_umax(__float_as_uint(
+                    fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y))))));
+                const int e = kv_clamp(int(__float_as_uint(amax) >> 23) - 127, -120, 120);
+                const float up = copysignf(__uint_as_float(uint32_t(127 - e) << 23), a.sm_scale);
+                if (lane == r0 + k) unscale = __uint_as_float(uint32_t(127 + e) << 23);
+                x[k] = make_uint2(act_t2<__half>(lo.x * up, lo.y * up), act_t2<__half>(hi.x * up, hi.y * up));
+            } else if (a.sm_scale < 0.f) {
+                x[k].x ^= 0x80008000u;
+                x[k].y ^= 0x80008000u;
+            }
+            if (d4 < DT) {
+                uint8_t *p = rows_sm + d4 / 64 * Layout<DT>::kAtom + (r0 + k) * 128 + (((d4 % 64 / 8) ^ (k & 7)) << 4) + d4 % 8 * 2;
+                *reinterpret_cast<uint2 *>(p) = x[k];
+            }
+        }
     }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.q_full);
 
     float m = -INFINITY, l = 0.f, vref = 0.f;
-    for (int j = 0; j < t.steps; ++j) {
+    for (int j = 0; j < steps; ++j) {
         const int set = j % kRing, key0 = j * kKeys;
         if (!wait_warp(&bar.sc_full[set], (j / kRing) & 1, abort) || !wait_warp(&bar.s_full[tile], j & 1, abort)) return;
         tc::fence_after_sync();
         const int left = seen - key0;  // keys of this step that the row sees
-        const bool plain = __all_sync(0xffffffffu, left >= kKeys) && sc.plain[set];
+        const int least = __reduce_min_sync(0xffffffffu, left);
+        // ---- One pass where the running references hold: no score too far over the maximum so far
+        // shows as no group of weights summing up to more than binary16 holds (weights under the
+        // maximum sum up to at most 16 * 2^kRaise = 2^15), so the sums that l needs anyway are the
+        // check.  The weights stay in registers until it passed.  The value scale is part of the
+        // exponent, P = 2^(x - m + kRaise + log2(vs / vref)), and l takes a group's sum back over
+        // vs / vref.
         const uint32_t dead = sc.dead[set];
-        // ---- maximum (loops over chunks of 32 keys stay loops: unrolled, the roles' code would not
-        // fit the instruction cache)
-        float mx = -INFINITY;
+        const bool all_seen = least >= kKeys, plain = sc.plain[set];
+        bool refer = j == 0 || !plain || !__all_sync(0xffffffffu, sc.v_max[set] < vref && (m > -INFINITY || left <= 0));
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tc::ld_32x32b_x32(scol + 32 * c, s);
-            tc::wait_ld();
+        for (;;) {
+            if (refer && !new_references<DT>(scol, ocol, sc, set, unscale, left, all_seen && !dead, dead, j, tile, bar, abort, m, vref, l))
+                return;
             if (!plain) {
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    if (32 * c + x >= left || (dead >> (2 * c + x / 16) & 1)) s[x] = 0xff800000u;  // -inf
+                weights_any(scol, sc, set, unscale, left, dead, m, vref, l);
+                break;
             }
-            float top[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float y[4];  // (scales are not negative: the largest product is the largest score's)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    y[x] = fmaxf(__uint_as_float(s[16 * h + x]), __uint_as_float(s[16 * h + 4 + x]));
-                    y[x] = fmaxf(fmaxf(y[x], __uint_as_float(s[16 * h + 8 + x])), __uint_as_float(s[16 * h + 12 + x]));
-                }
-                top[h] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            const float shift = kRaise - (m == -INFINITY ? 0.f : m) - float(int(__float_as_uint(vref) >> 23) - 127);
+            float lsum = 0.f;
+            const bool fits = all_seen
+                                  ? weights_once<false>(scol, sc.k[set], sc.log_v[set], sc.inv_v[set], unscale, shift, left, lsum, refer)
+                                  : weights_once<true>(scol, sc.k[set], sc.log_v[set], sc.inv_v[set], unscale, shift, left, lsum, refer);
+            if (fits) {
+                l = fmaf(lsum, vref, l);
+                break;
             }
-            // -inf stays -inf where a scale is 0
-            mx = fmaxf(mx, top[0] == -INFINITY ? top[0] : top[0] * (sc.k[set][2 * c] * unscale));
-            mx = fmaxf(mx, top[1] == -INFINITY ? top[1] : top[1] * (sc.k[set][2 * c + 1] * unscale));
+            refer = true;
         }
-        const float m_new = mx > m + kSlack ? mx : m;  // -inf until the row sees a key
-        // ---- reference of the value scales: a power of two above all so far
-        const float vmax = sc.v_max[set];
-        const float vnew = vmax >= vref && vmax > 0.f
-                               ? __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u) : vref;
-        const float inv = vnew > 0.f ? 1.f / vnew : 0.f;
-        const float fm = m_new == m ? 1.f : exp2_approx(m - m_new);
-        const float fo = vnew == vref ? fm : fm * (vref * inv);
-        l *= fm;
-        if (j > 0 && __any_sync(0xffffffffu, fo != 1.f)) {
-            if (!wait_warp(&bar.o_done[tile], (j - 1) & 1, abort)) return;
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < DT / 32; ++c) {
-                uint32_t o[32];
-                tc::ld_32x32b_x32(ocol + 32 * c, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
-                tc::st_32x32b_x32(ocol + 32 * c, o);
-            }
-            tc::wait_st();
-        }
-        m = m_new;
-        vref = vnew;
-        // ---- weights, over the scores that are already read
-        const float base = m == -INFINITY ? 0.f : m - kRaise;
-        if (plain) {
-            // the value scale as part of the exponent: P = 2^(x - base + log2(vs / vref)); the weight
-            // sum takes the group's sum back over vs / vref
-            const float log_ref = float(int(__float_as_uint(vref) >> 23) - 127);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t s[32], p[16];
-                tc::ld_32x32b_x32(scol + 32 * c, s);
-                tc::wait_ld();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int g = 2 * c + h;
-                    const float k = sc.k[set][g] * unscale, off = sc.log_v[set][g] - log_ref - base;
-                    const float2 k2 = make_float2(k, k), off2 = make_float2(off, off);
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int x = 0; x < 16; x += 2) {
-                        const float2 e = fma2(make_float2(__uint_as_float(s[16 * h + x]), __uint_as_float(s[16 * h + x + 1])), k2, off2);
-                        const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                        sum = add2(sum, w);
-                        p[8 * h + x / 2] = act_t2<__half>(w.x, w.y);
-                    }
-                    l = fmaf(sum.x + sum.y, vref * sc.inv_v[set][g], l);
-                }
-                tc::st_32x32b_x16(scol + 16 * c, p);
-            }
-        } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t s[32], p[16];
-                tc::ld_32x32b_x32(scol + 32 * c, s);
-                tc::wait_ld();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int g = 2 * c + h;
-                    const float k = sc.k[set][g] * unscale, v = sc.v[set][g] * inv;
-                    const bool gone = dead >> g & 1;
-#pragma unroll
-                    for (int x = 0; x < 16; x += 2) {
-                        float w[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int at = 16 * h + x + e;
-                            w[e] = exp2_approx(fmaf(__uint_as_float(s[at]), k, -base));
-                            if (32 * c + at >= left || gone) w[e] = 0.f;
-                        }
-                        l += w[0] + w[1];
-                        p[8 * h + x / 2] = act_t2<__half>(w[0] * v, w[1] * v);
-                    }
-                }
-                tc::st_32x32b_x16(scol + 16 * c, p);
-            }
-        }
-        tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[tile]);
     }
-    if (t.steps > 0 && !wait_warp(&bar.o_done[tile], (t.steps - 1) & 1, abort)) return;
+    if (steps > 0 && !wait_warp(&bar.o_done[tile], (steps - 1) & 1, abort)) return;
     tc::fence_after_sync();
+    // ---- the finished rows: through the warp's part of the query rows' memory (its products are
+    // done), so that rows leave as whole lines
     const float inv = l > 0.f ? vref / l : (l == l ? 0.f : l);
-    uint16_t *out = static_cast<uint16_t *>(a.out) + at;
-#pragma unroll
+    uint8_t *back = qsm + tile * Layout<DT>::kQ + 32 * (warp % 4) * (2 * DT);
+    if (steps == 0) named_bar_sync(1 + tile, kTile);  // (no product said that all query rows are written)
+#pragma unroll 1
     for (int c = 0; c < DT / 32; ++c) {
         uint32_t o[32];
-        if (t.steps > 0) {
+        if (steps > 0) {
             tc::ld_32x32b_x32(ocol + 32 * c, o);
             tc::wait_ld();
         }
 #pragma unroll
-        for (int x = 0; x < 32; x += 4)
-            if (live && 32 * c + x < a.head_dim) {
-                float y[4];
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[x + e]) * inv;
-                *reinterpret_cast<uint2 *>(out + 32 * c + x) = make_uint2(act_t2<T>(y[0], y[1]), act_t2<T>(y[2], y[3]));
+            for (int e = 0; e < 4; ++e) {
+                const float x = l == 0.f ? 0.f : __uint_as_float(o[8 * k + 2 * e]) * inv;
+                const float y = l == 0.f ? 0.f : __uint_as_float(o[8 * k + 2 * e + 1]) * inv;
+                h[e] = act_t2<T>(x, y);
             }
+            sts128(back + lane * (2 * DT) + (((4 * c + k) ^ (lane & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+        }
+    }
+    __syncwarp();
+#pragma unroll 8
+    for (int k = 0; k < 32; ++k) {
+        const int64_t to = __shfl_sync(0xffffffffu, at, k);
+        if ((lives >> k & 1) && d4 < a.head_dim)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to + d4) =
+                lds64(back + k * (2 * DT) + (((d4 / 8) ^ (k & 7)) << 4) + d4 % 8 * 2);
     }
 }
 
@@ -573,8 +641,8 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     uint8_t *kraw = vsm + 2 * Layout<DT>::kV, *vraw = kraw + Layout<DT>::kRaw;
     volatile int *abort = &abort_flag;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    grid_dep_launch();
     grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
+    grid_dep_launch();  // (not before: see KvAttnArgs::behind_tiles)
 
     const int64_t item = blockIdx.x / a.kv_heads;
     if (tid == 0) {
@@ -608,6 +676,9 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     t.keys = max(0, t.s.len - t.s.n + (t.row0 + t.rows - 1) / a.group + 1);
     t.steps = (t.keys + kKeys - 1) / kKeys;
     t.tiles = t.rows > kTile ? 2 : 1;
+    const int first_keys = max(0, t.s.len - t.s.n + (t.row0 + min(t.rows, kTile) - 1) / a.group + 1);
+    t.steps_of[0] = (first_keys + kKeys - 1) / kKeys;
+    t.steps_of[1] = t.steps;
 
     if (tid == 0) {
         mbar_init(&bar.q_full, 4 * t.tiles);
