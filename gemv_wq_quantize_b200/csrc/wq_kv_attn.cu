@@ -1,24 +1,30 @@
 // wq_kv_attn.cu -- kv_attention: the C entry points, and the kernel for few rows per key head
 // (decode and draft verification): attention over the paged 8-bit cache, split over the whole
-// GPU by key ranges.
+// GPU by key ranges, on the 5th-generation tensor cores (tcgen05) without widening a code.
 //
 // Mathematics: for a query row q of position p and the keys j <= p of its sequence,
 //   s_j = sm_scale * ks[page(j)] * (q . kc_j),   out = sum_j softmax(s)_j vs[page(j)] vc_j
-// with the codes kc, vc exact in binary16, products on mma.sync with binary32 accumulation, one
-// pass with a running maximum and sum, and the two page scales applied in binary32.
+// with a running maximum and sum, and the two page scales applied in binary32.
 //
-// Bound by reading the cache once.  A group of query heads shares a key head's codes, so the rows
-// of (sequence, key head) form the 8-wide N side of both products (S^T = K Q^T and
-// O^T = V^T P^T): the codes are the 16-row A operand and nothing is wasted on padding up to 8
-// rows (an M side of 128 rows of tcgen05 would be 8 of 128 full).  Every warp walks its own keys
-// with a small ring of its own: TMA copies of 32 keys or values (16 at head sizes above 128) into
-// swizzled shared memory, the next ones issued by the warp as soon as it has read a buffer, so
-// two are in flight while it multiplies a third and no warp waits for another between the ends of
-// a tile.  The swizzle makes the fragment reads free of bank conflicts; a dot product may take its
-// dimensions in any order, so a lane's 16 contiguous bytes of a key are its fragments of four MMA
-// steps, and its 16 contiguous bytes of four values are its fragments of eight row tiles.
+// Bound by reading the cache once; widening the codes to binary16 in registers took 850
+// instructions a warp for 32 keys and held the reads to 4.7 TB/s.  So the codes are MMA operands as
+// they lie in memory, and the few rows are cut into 8-bit parts instead:
+//   q = 2^e (q1 + q2 / 16 + q3 / 256 + q4 / 4096)      e4m3 cache: each part the e4m3 value nearest
+//                                                       to what is left
+//   q = 2^e (q1 2^21 + q2 2^14 + q3 2^7 + q4)           INT8 cache: digits of a 28-bit integer
+// (exact for binary16 and bfloat16 down to 2^-27 of the row's largest value), and the weights in
+// [0, 1) likewise, to 2^-29.  The parts of all rows are the N side of both products,
+//   S^T[key][part, row] = K Q^T      A = 128 keys of codes (rows of dimensions),
+//   O^T[dimension][part, row] = V^T P^T      A = the values of 128 keys, read dimension-major,
+// with binary32 (e4m3) or exact int32 (INT8) accumulators in Tensor Memory, and the parts are put
+// together in binary32 when a step's scores or sums are read back.
+//  * warps 0-3: a thread per key for the softmax (maxima over the warps through shared memory),
+//    and a thread per dimension for the output, which is added up in registers step by step;
+//  * warp 4: one thread issues the MMAs, the next step's scores in front of this step's sums;
+//  * warp 5: fills a ring of stages of 128 keys and values by TMA, page by page, and their scales.
+// Every wait is bounded; on expiry the block records an error, stops and frees its Tensor Memory.
 //
-// Work split: tiles (sequence, key head, 8 * NT rows) are cut into units of 64 keys, and the
+// Work split: tiles (sequence, key head, 8 or 16 rows) are cut into units of 128 keys, and the
 // persistent blocks take equal contiguous shares of all units, whatever the lengths (a tile counts
 // kTileUnits more, about what its start and end take).  A tile cut over several blocks leaves
 // partial sums in the workspace; the last block to arrive adds them in the order of their keys,
@@ -32,6 +38,7 @@
 
 #include "wq_act.cuh"
 #include "wq_kv_attn.cuh"
+#include "wq_tc.cuh"
 
 namespace wq {
 
@@ -47,24 +54,15 @@ int kv_attn_read_error()
 
 namespace {
 
-constexpr int kWarps = 6;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kUnitShift = 6;     // a unit: 64 keys, the granule of the split
-constexpr int kTileUnits = 6;     // what the start and end of a tile cost a block, in units
-constexpr int kLeastUnits = 4;    // of a share: a stage for each warp; less only adds partials
+constexpr int kKeys = 128;               // keys of a step: MMA M of the scores
+constexpr int kGroups = kKeys / 16;      // a group of 16 keys lies in one page
+constexpr int kSoft = 128;               // threads of the softmax warps
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kThreads = 192;
+constexpr int kParts = 4;                // 8-bit parts of a query value or weight
+constexpr int kUnitShift = 7;            // a unit: 128 keys, the granule of the split
+constexpr int kTileUnits = 4;            // what the start and end of a tile cost a block, in units
+constexpr int kLeastUnits = 1;           // of a share: less only adds partials
 constexpr int kMostUnits = 1 << 30;
-
-// exp2 arguments are raised by 15: the weights then reach 2^15 in binary16 (its largest is just
-// below 2^16) and keep full precision down to 2^-29 of the largest weight, so that many small
-// weights under one large one are not lost; the sum carries the same factor.
-constexpr float kRaise = 15.f;
-
-__device__ __forceinline__ uint32_t trans8x8(uint32_t x)
-{
-    uint32_t d;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
-    return d;
-}
 
 __device__ __forceinline__ uint64_t globaltimer()
 {
@@ -73,214 +71,141 @@ __device__ __forceinline__ uint64_t globaltimer()
     return t;
 }
 
-// DT: head_dim rounded up to 64, 128 or 256.  NT: tiles of 8 rows.
-template <int DT, int NT>
+// NB: boxes of 128 dimensions (1 up to a head size of 128, 2 up to 256).  NR: rows of a tile.
+template <int NB, int NR>
 struct Shape {
-    static constexpr int kRows = 8 * NT;
-    static constexpr int kPerSm = DT <= 128 && NT == 1 ? 2 : 1;  // blocks: 128 or 255 registers a thread
-    static constexpr int kSteps = DT <= 128 ? 2 : 1;             // 16-key steps of a stage
-    static constexpr int kKeys = 16 * kSteps;
-    static constexpr int kRowBytes = DT < 128 ? 64 : 128;        // of a copied box; two boxes at DT 256
-    static constexpr int kBoxes = DT / 128 < 1 ? 1 : DT / 128;
-    static constexpr int kBoxBytes = kKeys * kRowBytes;
-    static constexpr int kItem = kBoxBytes * kBoxes;             // the keys (or values) of a stage
-    static constexpr int kBufs = kPerSm == 2 ? 4 : 5;            // items of a warp's ring
-    static constexpr int kRowFloats = DT + 4;                    // a partial row: sums, maximum, weight sum
+    static constexpr int kN = kParts * NR;               // MMA N
+    static constexpr int kBox = kKeys * 128;             // bytes of 128 keys x 128 dimensions
+    static constexpr int kPerSm = NB == 1 ? 2 : 1;       // blocks
+    static constexpr int kStages = NR == 8 ? 3 : 2;      // 96 KB (64 KB) of a block's share of an SM
+    static constexpr int kRowFloats = 128 * NB + 4;      // a partial row: sums, maximum, weight sum
+    static constexpr uint32_t kSCol = 0, kOCol = 2 * kN; // two of each: scores [2], sums [2][NB]
+    static constexpr uint32_t kUsed = 2 * kN * (1 + NB), kTmem = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
 
-// A row of sums in shared memory and in the workspace is kept in the order of the fragments:
-// place 16 i + 2 g + e holds dimension dim_of(that) (lane (g, j) then stores pairs without bank
-// conflicts, rows being DT + 4 apart).
-template <int DT>
-__device__ __forceinline__ int dim_of(int place)
-{
-    const int i = place / 16, g = place % 16 / 2, e = place % 2;
-    return DT == 64 ? 8 * g + 2 * i + e : 128 * (i / 8) + 16 * g + 2 * (i % 8) + e;
-}
-
-template <int DT, int NT>
+template <int NB, int NR>
 struct Smem {
-    using S = Shape<DT, NT>;
-    alignas(1024) uint8_t ring[kWarps][S::kBufs][S::kItem];
-    uint64_t full[kWarps][S::kBufs];
-    float o[kWarps][8 * NT][DT / 4 + 4];   // a quarter of the warps' sums at a time
-    float m[kWarps][8 * NT], l[kWarps][8 * NT], f[kWarps][8 * NT];
-    float top[8 * NT], weight[8 * NT];     // of a row over the warps
-    int64_t sums[kWarps];
-    int first[2], parts[2];                // the tiles that this block left partials of
+    using S = Shape<NB, NR>;
+    alignas(1024) uint8_t k[S::kStages][NB][S::kBox];
+    alignas(1024) uint8_t v[S::kStages][NB][S::kBox];
+    alignas(1024) uint8_t q[NB][S::kN * 128];  // rows (part, row) of 128 dimensions
+    alignas(1024) uint8_t p[2][S::kN * 128];   // rows (part, row) of 128 keys
+    uint64_t full[S::kStages], empty[S::kStages], scales[S::kStages], s_full[2], p_full[2], o_full[2], q_full, joined;
+    float ks[S::kStages][kGroups], vs[S::kStages][kGroups], v_max[S::kStages];
+    uint32_t dead[S::kStages];   // groups whose block-table entry is no page
+    float q_scale[NR];           // of a row's parts, times sm_scale and log2 e
+    int seen[NR];                // keys that a row sees (0: no row)
+    int64_t row_at[NR];          // its first element in q and out
+    alignas(16) int top[2][NR][4];    // the warps' maxima of a step (order_of)
+    float sum[4][NR];            // the warps' weight sums of a tile
+    int64_t units[kThreads / 32];
+    int first[2], parts[2];      // the tiles that this block left partials of
     int abort;
+    uint32_t tmem;
     // then the unit counts of all sequences up to each (n_seqs + 1)
 };
 
-// A bounded wait with one answer for the warp: about 2 s, or 20 ms once another warp gave up.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort)
+// A bounded wait: about 2 s, or `after` (nanoseconds) once another role gave up.  wait_warp: one
+// answer for the warp.  The softmax warps go on after a wait that gave up, so that they reach the
+// same barriers as often; what they then write is not valid.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t after = 100000)
 {
-    bool ok = false;
-    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait_short(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = globaltimer();
-        while (!ok) {
-            for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait_short(bar, parity);
-            if (!ok && globaltimer() - t0 > (*abort ? 20000000ull : 2000000000ull)) {
-                atomicCAS(&g_kv_attn_error, kErrNone, kErrWaitTimeout);
-                *abort = 1;
-                break;
-            }
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait_short(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait_short(bar, parity)) return true;
+        if (globaltimer() - t0 > (*abort ? after : 2000000000ull)) {
+            atomicCAS(&g_kv_attn_error, kErrNone, kErrWaitTimeout);
+            *abort = 1;
+            return false;
         }
     }
-    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t after = 100000)
+{
+    return __all_sync(0xffffffffu, wait(bar, parity, abort, after));
 }
 
-// The codes of 16 keys of a stage in the registers of a warp, from swizzled shared memory.
-// Keys: lane (g, j) has keys g and g + 8, dimensions kdim(c, j) .. + 15.
-template <int DT>
-__device__ __forceinline__ int kdim(int c, int j)
+template <bool F8>
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    return DT == 64 ? 16 * j : 128 * (c / 2) + 32 * j + 16 * (c % 2);
+    if constexpr (F8) tc::mma_f8_ss(d, a, b, idesc, accumulate);
+    else tc::mma_i8_ss(d, a, b, idesc, accumulate);
 }
-template <int DT, int NT>
-__device__ __forceinline__ uint4 key_chunk(const uint8_t *k, int row, int c, int j)
+
+// The parts of four values x (e4m3: |x| < 448, each part the value nearest to sixteen times what
+// the ones before left; INT8: x an integer below 2^28 in magnitude, 7 bits a digit, the first with
+// the sign), as bytes of a word per part.
+template <bool F8>
+__device__ __forceinline__ void split4(const float (&x)[4], uint32_t (&part)[kParts])
 {
-    if constexpr (DT == 64) return lds128(k + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
-    else return lds128(k + c / 2 * Shape<DT, NT>::kBoxBytes + row * 128 + (((2 * j + c % 2) ^ (row & 7)) << 4));
-}
-// Values: lane (g, j) has keys 2j, 2j + 1, 2j + 8, 2j + 9 and DT / 8 bytes of each.
-template <int DT, int NT>
-__device__ __forceinline__ void value_words(const uint8_t *v, int row, int g, uint32_t (&w)[DT / 32])
-{
-    if constexpr (DT == 64) {
-        const uint2 x = lds64(v + row * 64 + (((g / 2) ^ ((row >> 1) & 3)) << 4) + 8 * (g % 2));
-        w[0] = x.x;
-        w[1] = x.y;
+    if constexpr (F8) {
+        float r[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            const uint32_t w = e4m3x4(r[0], r[1], r[2], r[3]);
+            part[p] = w;
+            if (p + 1 < kParts)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = (r[i] - code_value<true>(w, i)) * 16.f;
+        }
     } else {
+        uint32_t u[4];
 #pragma unroll
-        for (int c = 0; c < DT / 128; ++c) {
-            const uint4 x = lds128(v + c * Shape<DT, NT>::kBoxBytes + row * 128 + ((g ^ (row & 7)) << 4));
-            w[4 * c] = x.x;
-            w[4 * c + 1] = x.y;
-            w[4 * c + 2] = x.z;
-            w[4 * c + 3] = x.w;
+        for (int i = 0; i < 4; ++i) u[i] = uint32_t(__float2int_rn(x[i]));
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = p == 0 ? uint32_t(int32_t(u[i]) >> 21) : (u[i] >> (21 - 7 * p)) & 127u;
+            part[p] = prmt(prmt(b[0], b[1], 0x0040), prmt(b[2], b[3], 0x0040), 0x5410);
         }
     }
 }
-
-// One warp's running state over its keys: column n of the products is row n of the tile.
-template <int DT, int NT>
-struct State {
-    float o[NT][DT / 16][4];  // lane (g, j): places 16 i + 2 g and + 1; rows 2j, 2j + 1
-    float m[NT][2], l[NT][2];
-};
-
-// Queries as B fragments (binary16): k-step 4 c + w holds, for lane (g, j) and row g, the
-// dimensions kdim(c, j) + 4 w .. + 3.  A bfloat16 row is scaled by a power of two so that its
-// largest value fits binary16; what falls below the smallest subnormal there is under 2^-25 of
-// the row's largest value, the size of the binary32 accumulation's own rounding.  The scale's
-// inverse comes back for rows 2j and 2j + 1.
-template <bool BF16, int DT, int NT>
-__device__ __forceinline__ void load_queries(const KvAttnArgs &a, const KvSpan &s, int head, int row0, int rows, int g,
-                                             int j, uint32_t (&qf)[NT][DT / 16][2], float (&unscale)[NT][2])
+// The value of accumulated parts, in units of the first (e4m3) or the last (INT8).
+template <bool F8>
+__device__ __forceinline__ float whole_of(uint32_t c1, uint32_t c2, uint32_t c3, uint32_t c4)
 {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int r = row0 + 8 * n + g;
-        const bool live = 8 * n + g < rows;
-        const int i = live ? r / a.group : 0, h = live ? r % a.group : 0;
-        const uint16_t *q = static_cast<const uint16_t *>(a.q) +
-                            (int64_t(s.q0 + i) * a.q_heads + head * a.group + h) * a.head_dim;
-        float amax = 0.f;
-#pragma unroll
-        for (int c = 0; c < DT / 64; ++c)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int d = kdim<DT>(c, j) + 4 * w;
-                const uint2 x = live && d < a.head_dim ? *reinterpret_cast<const uint2 *>(q + d) : make_uint2(0, 0);
-                qf[n][4 * c + w][0] = x.x;
-                qf[n][4 * c + w][1] = x.y;
-                if constexpr (BF16) {
-                    const float2 lo = act_f2<__nv_bfloat16>(x.x), hi = act_f2<__nv_bfloat16>(x.y);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y))));
-                }
-            }
-        unscale[n][0] = unscale[n][1] = 1.f;
-        if constexpr (BF16) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // 2^-e with e the exponent of the largest value: the row's values stay within 2
-            const int e = kv_clamp(int(__float_as_uint(amax) >> 23) - 127, -120, 120);
-            const float up = __uint_as_float(uint32_t(127 - e) << 23), down = __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-            for (int k = 0; k < DT / 16; ++k)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float2 v = act_f2<__nv_bfloat16>(qf[n][k][x]);
-                    qf[n][k][x] = act_t2<__half>(v.x * up, v.y * up);
-                }
-            unscale[n][0] = __shfl_sync(0xffffffffu, down, 8 * j);       // row 2j is lane (2j, 0)
-            unscale[n][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4);
-        }
-    }
+    if constexpr (F8)
+        return fmaf(fmaf(fmaf(__uint_as_float(c4), 0.0625f, __uint_as_float(c3)), 0.0625f, __uint_as_float(c2)), 0.0625f,
+                    __uint_as_float(c1));
+    else
+        return fmaf(float(int(c1)), 2097152.f, fmaf(float(int(c2)), 16384.f, fmaf(float(int(c3)), 128.f, float(int(c4)))));
+}
+// Exponents: a query row with largest value 2^e .. 2^(e+1) is multiplied by 2^(kQUp - e) before it
+// is cut; a weight, at most 2^kSlack and under its reference's value scale, by kPUp (to at most
+// 256, or 2^28).  A maximum that rises by less than kSlack is not followed.
+constexpr float kSlack = 2.f;
+template <bool F8>
+constexpr int kQUp = F8 ? 7 : 26;
+template <bool F8>
+constexpr float kPUp = F8 ? 64.f : 67108864.f;
+
+// A power of two's inverse (normal, and so is the inverse).
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
+
+// Whether any thread of the softmax warps has the predicate: their barrier and the answer in one.
+__device__ __forceinline__ bool soft_any(bool mine)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(uint32_t(mine)), "n"(kSoft)
+        : "memory");
+    return any != 0;
 }
 
-// Scores of 16 keys (rows row0 .. + 15 of a stage): S^T[key][row], lane (g, j) holds keys g and
-// g + 8, rows 2j and 2j + 1.
-template <bool F8, int DT, int NT>
-__device__ __forceinline__ void scores(const uint8_t *k, int row0, int g, int j, const uint32_t (&qf)[NT][DT / 16][2], float (&s)[NT][4])
+// Signed integers in the order of the floats (NaN above all), for the warp-wide integer maximum.
+__device__ __forceinline__ int order_of(float x)
 {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
-#pragma unroll
-    for (int c = 0; c < DT / 64; ++c) {
-        const uint4 r0 = key_chunk<DT, NT>(k, row0 + g, c, j), r1 = key_chunk<DT, NT>(k, row0 + g + 8, c, j);
-        const uint32_t lo[4] = {r0.x, r0.y, r0.z, r0.w}, hi[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t x = F8 ? lo[w] : lo[w] ^ 0x80808080u, y = F8 ? hi[w] : hi[w] ^ 0x80808080u;
-            const uint32_t f[4] = {widen<F8, 0>(x), widen<F8, 0>(y), widen<F8, 1>(x), widen<F8, 1>(y)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(s[n], f, qf[n][4 * c + w][0], qf[n][4 * c + w][1]);
-        }
-    }
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
 }
-
-// O^T += vs * (V^T P^T) over 16 keys; p: the weights as B fragments.  left: keys of the 16 that
-// hold codes (the slots behind may hold e4m3 NaN codes).
-template <bool F8, int DT, int NT>
-__device__ __forceinline__ void add_values(const uint8_t *v, int row0, int left, int g, int j,
-                                           const uint32_t (&p)[NT][2], float vs, State<DT, NT> &st)
-{
-    uint32_t w[4][DT / 32];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int key = 2 * j + (t & 1) + 8 * (t >> 1);
-        value_words<DT, NT>(v, row0 + key, g, w[t]);
-        if (F8 && left < 16 && key >= left)
-#pragma unroll
-            for (int x = 0; x < DT / 32; ++x) w[t][x] = 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < DT / 16; i += 2) {
-        // bytes 2i .. 2i + 3 of the lane's chunk of four keys: row tiles i and i + 1
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            uint32_t a = prmt(w[0][i / 2], w[1][i / 2], e ? 0x7362 : 0x5140);
-            uint32_t b = prmt(w[2][i / 2], w[3][i / 2], e ? 0x7362 : 0x5140);
-            if constexpr (!F8) {
-                a ^= 0x80808080u;
-                b ^= 0x80808080u;
-            }
-            const uint32_t f[4] = {widen<F8, 0>(a), widen<F8, 1>(a), widen<F8, 0>(b), widen<F8, 1>(b)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(acc, f, p[n][0], p[n][1]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) st.o[n][i + e][x] = fmaf(vs, acc[x], st.o[n][i + e][x]);
-            }
-        }
-    }
-}
+__device__ __forceinline__ float of_order(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 struct Tile {
     KvSpan s;
@@ -310,7 +235,7 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs &a, const int *before, 
     t.s = kv_span(__ldg(a.cu_q + lo), __ldg(a.cu_q + lo + 1), __ldg(a.seq_len + lo), a.M, a.capacity);
     const bool split = a.partials != nullptr;
     const int head_units = split ? kTileUnits : 0;
-    const int units = split ? head_units + int(kv_units(t.s.len, 1 << shift)) : 1;
+    const int units = split ? head_units + max(1, int((int64_t(t.s.len) + (1 << shift) - 1) >> shift)) : 1;  // kv_units
     const int tiles = (t.s.n * a.group + ROWS - 1) / ROWS;
     const int item = (u - before[lo]) / units;  // (key head, tile) of the sequence
     const int begin = before[lo] + item * units, end = begin + units;
@@ -333,223 +258,6 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs &a, const int *before, 
     return t;
 }
 
-// A warp's walk over its stages of a tile (every kWarps-th) with its ring of items (keys and values
-// of its stages in turn).  begin() looks up the pages and sends for the first items; run() takes
-// them in.  Between the two a block joins the sums of its tile before, while the copies travel.
-template <int DT, int NT>
-struct Walk {
-    using S = Shape<DT, NT>;
-    struct Pages {  // lane l has those of the warp's stage base + l
-        int z[2];   // (page, head) of the stage's boxes; -1: none; -2: no page
-        float ks[S::kSteps], vs[S::kSteps];
-    };
-    const KvAttnArgs &a;
-    const CUtensorMap *km, *vm;
-    Smem<DT, NT> &sm;
-    Tile t;
-    Pages cur, next;
-    int mine;        // the warp's stages: warp + i * kWarps
-    int base;        // the stage that lane 0's pages are for
-    int issued;      // items
-    uint32_t item0;  // items of the warp over all tiles before: item x goes to buffer (item0 + x) % kBufs
-
-    __device__ __forceinline__ Walk(const KvAttnArgs &a_, const CUtensorMap *km_, const CUtensorMap *vm_, Smem<DT, NT> &sm_)
-        : a(a_), km(km_), vm(vm_), sm(sm_), mine(0), item0(0)
-    {
-    }
-    __device__ __forceinline__ int box_rows() const { return min(1 << a.page_shift, S::kKeys); }
-    __device__ __forceinline__ bool two() const { return (1 << a.page_shift) < S::kKeys; }  // a stage lies in two pages
-    __device__ __forceinline__ int key_of(int i) const { return t.t0 + (int(threadIdx.x) / 32 + i * kWarps) * S::kKeys; }
-
-    __device__ __forceinline__ void look_up(Pages &p, int i)
-    {
-        const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int key = key_of(i) + x * 16;
-            p.z[x] = -1;
-            if (i < mine && key < t.t1 && (x == 0 || two())) {
-                const int64_t page = kv_page_ok(__ldg(table + (key >> a.page_shift)), a.num_pages);
-                p.z[x] = page < 0 ? -2 : int(page) * a.kv_heads + t.head;
-            }
-        }
-    }
-    __device__ __forceinline__ void look_up_scales(Pages &p)
-    {
-#pragma unroll
-        for (int e = 0; e < S::kSteps; ++e) {
-            const int z = two() && e ? p.z[1] : p.z[0];
-            p.ks[e] = z >= 0 ? __ldg(a.k_scale + z) : 0.f;
-            p.vs[e] = z >= 0 ? __ldg(a.v_scale + z) : 0.f;
-        }
-    }
-    __device__ __forceinline__ void issue()
-    {
-        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-        const int x = issued++, i = x / 2 - base;
-        const int z0 = __shfl_sync(0xffffffffu, i < 32 ? cur.z[0] : next.z[0], i % 32);
-        const int z1 = __shfl_sync(0xffffffffu, i < 32 ? cur.z[1] : next.z[1], i % 32);
-        if (lane == 0) {
-            const uint32_t b = (item0 + x) % S::kBufs;
-            uint8_t *dst = sm.ring[warp][b];
-            uint64_t *bar = &sm.full[warp][b];
-            const CUtensorMap *map = x & 1 ? vm : km;
-            const uint32_t bytes = uint32_t(box_rows() * S::kRowBytes * S::kBoxes);
-            mbar_arrive_expect_tx(bar, (z0 >= 0 ? bytes : 0u) + (z1 >= 0 ? bytes : 0u));
-            const int y = two() ? 0 : key_of(x / 2) & ((1 << a.page_shift) - 1);
-#pragma unroll
-            for (int c = 0; c < S::kBoxes; ++c) {
-                if (z0 >= 0) tma_load_3d(dst + c * S::kBoxBytes, map, 128 * c, y, z0, bar);
-                if (z1 >= 0) tma_load_3d(dst + c * S::kBoxBytes + 16 * S::kRowBytes, map, 128 * c, 0, z1, bar);
-            }
-            if (z0 == -2 || z1 == -2) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
-        }
-    }
-    __device__ __forceinline__ bool ready(int x)
-    {
-        return wait_warp(&sm.full[threadIdx.x / 32][(item0 + x) % S::kBufs], ((item0 + x) / S::kBufs) & 1, &sm.abort);
-    }
-
-    // All items of the tile before are taken in (the ring is free).
-    __device__ __forceinline__ void begin(const Tile &tile)
-    {
-        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-        item0 += 2u * uint32_t(mine);
-        t = tile;
-        const int n = (t.t1 - t.t0 + S::kKeys - 1) / S::kKeys;  // stages of the tile
-        mine = max(0, n - warp + kWarps - 1) / kWarps;
-        base = issued = 0;
-        if (mine == 0) return;
-        look_up(cur, lane);
-        look_up_scales(cur);  // in front of the copies, which would delay them
-#pragma unroll 1
-        while (issued < min(int(S::kBufs), 2 * mine)) issue();
-        look_up(next, 32 + lane);
-    }
-    template <bool F8, bool BF16>
-    __device__ __forceinline__ void run(State<DT, NT> &st);
-};
-
-template <int DT, int NT>
-template <bool F8, bool BF16>
-__device__ __forceinline__ void Walk<DT, NT>::run(State<DT, NT> &st)
-{
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, j = lane % 4;
-#pragma unroll
-    for (int r = 0; r < NT; ++r) {
-        st.m[r][0] = st.m[r][1] = -INFINITY;
-        st.l[r][0] = st.l[r][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < DT / 16; ++i)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) st.o[r][i][x] = 0.f;
-    }
-    if (mine == 0) return;
-    const int items = 2 * mine;
-    uint32_t qf[NT][DT / 16][2];
-    float qs[NT][2];
-    load_queries<BF16, DT, NT>(a, t.s, t.head, t.row0, t.rows, g, j, qf, qs);
-    int seen[NT][2];  // keys that rows 2j and 2j + 1 see
-#pragma unroll
-    for (int r = 0; r < NT; ++r)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int row = 8 * r + 2 * j + x;
-            seen[r][x] = row < t.rows ? min(t.t1, t.s.len - t.s.n + (t.row0 + row) / a.group + 1) : 0;
-            qs[r][x] *= a.sm_scale * kLog2e;
-        }
-    const int least = min(t.t1, t.s.len - t.s.n + t.row0 / a.group + 1);  // keys that every row sees
-
-    const bool pair = two();
-    int done = 0;  // items waited for
-    for (int i = 0; i < mine; ++i) {
-        if (i - base == 32) {
-            base += 32;
-            cur = next;
-            look_up(next, base + 32 + lane);
-        }
-        if (i - base == 8) look_up_scales(next);
-        const int key = key_of(i);
-        float s[S::kSteps][NT][4], vs[S::kSteps];
-        const uint8_t *k = sm.ring[warp][(item0 + 2 * i) % S::kBufs], *v = sm.ring[warp][(item0 + 2 * i + 1) % S::kBufs];
-        if (!ready(done++)) break;
-#pragma unroll
-        for (int e = 0; e < S::kSteps; ++e) {
-            scores<F8, DT, NT>(k, 16 * e, g, j, qf, s[e]);
-            const float ks = __shfl_sync(0xffffffffu, cur.ks[e], i - base);
-            vs[e] = __shfl_sync(0xffffffffu, cur.vs[e], i - base);
-            const int z = __shfl_sync(0xffffffffu, pair && e ? cur.z[1] : cur.z[0], i - base);
-#pragma unroll
-            for (int r = 0; r < NT; ++r)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[e][r][x] *= ks * qs[r][x & 1];
-            const int first = key + 16 * e;
-            if (first + 16 > least || z < 0) {
-#pragma unroll
-                for (int r = 0; r < NT; ++r)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (first + g + 8 * (x >> 1) >= seen[r][x & 1] || z < 0) s[e][r][x] = -INFINITY;
-            }
-        }
-        __syncwarp();  // the keys are read: their buffer takes the next item
-        if (issued < items) issue();
-        uint32_t p[S::kSteps][NT][2];
-#pragma unroll
-        for (int r = 0; r < NT; ++r) {
-            float mx[2] = {st.m[r][0], st.m[r][1]};
-#pragma unroll
-            for (int e = 0; e < S::kSteps; ++e)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mx[x & 1] = fmaxf(mx[x & 1], s[e][r][x]);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-            }
-            if (__any_sync(0xffffffffu, mx[0] > st.m[r][0] || mx[1] > st.m[r][1])) {
-                // -inf - -inf: no key seen yet, nothing to rescale
-                const float f0 = mx[0] == st.m[r][0] ? 1.f : exp2_approx(st.m[r][0] - mx[0]);
-                const float f1 = mx[1] == st.m[r][1] ? 1.f : exp2_approx(st.m[r][1] - mx[1]);
-                st.l[r][0] *= f0;
-                st.l[r][1] *= f1;
-#pragma unroll
-                for (int c = 0; c < DT / 16; ++c) {
-                    st.o[r][c][0] *= f0;
-                    st.o[r][c][1] *= f1;
-                    st.o[r][c][2] *= f0;
-                    st.o[r][c][3] *= f1;
-                }
-                st.m[r][0] = mx[0];
-                st.m[r][1] = mx[1];
-            }
-            const float low[2] = {mx[0] == -INFINITY ? 0.f : mx[0] - kRaise, mx[1] == -INFINITY ? 0.f : mx[1] - kRaise};
-#pragma unroll
-            for (int e = 0; e < S::kSteps; ++e) {
-                float w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    w[x] = exp2_approx(s[e][r][x] - low[x & 1]);
-                    st.l[r][x & 1] += w[x];
-                }
-                // weights to binary16: half a step is 2^-12 of each, of either sign
-                p[e][r][0] = trans8x8(act_t2<__half>(w[0], w[1]));
-                p[e][r][1] = trans8x8(act_t2<__half>(w[2], w[3]));
-            }
-        }
-        if (!ready(done++)) break;
-#pragma unroll
-        for (int e = 0; e < S::kSteps; ++e) {
-            const int z = __shfl_sync(0xffffffffu, pair && e ? cur.z[1] : cur.z[0], i - base);
-            add_values<F8, DT, NT>(v, 16 * e, z < 0 ? 0 : t.t1 - (key + 16 * e), g, j, p[e], vs[e], st);
-        }
-        __syncwarp();
-        if (issued < items) issue();
-    }
-    // (only after a wait gave up: nothing may land in memory that is used for something else)
-    while (done < issued) ready(done++);
-}
-
 __device__ __forceinline__ uint16_t *out_row(const KvAttnArgs &a, const Tile &t, int r)
 {
     const int row = t.row0 + r;
@@ -559,119 +267,452 @@ __device__ __forceinline__ uint16_t *out_row(const KvAttnArgs &a, const Tile &t,
 __device__ __forceinline__ float inverse_of(float l) { return l > 0.f ? 1.f / l : (l == l ? 0.f : l); }
 __device__ __forceinline__ float weight_of(float m, float top) { return m == -INFINITY ? 0.f : exp2_approx(m - top); }
 
-// The warps' states of a tile joined, a quarter of the places at a time: finished rows, or this
-// block's partial in `slot`.
-template <typename T, int DT, int NT>
-__device__ __forceinline__ void join(const KvAttnArgs &a, Smem<DT, NT> &sm, const Tile &t, State<DT, NT> &st, float *slot)
-{
-    using S = Shape<DT, NT>;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, j = lane % 4;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) {
-            st.l[n][0] += __shfl_xor_sync(0xffffffffu, st.l[n][0], o);
-            st.l[n][1] += __shfl_xor_sync(0xffffffffu, st.l[n][1], o);
+// A block's share of the units: its parts of tiles, one after the other (every role walks them).
+template <int NR>
+struct Share {
+    const KvAttnArgs &a;
+    const int *before;
+    int shift, u, u_end;
+    __device__ __forceinline__ bool next(Tile &t)
+    {
+        while (u < u_end) {
+            int behind;
+            t = tile_of<NR>(a, before, shift, u, u_end, behind);
+            u = behind;
+            if (behind > t.u0) return true;  // (else none of the tile's keys)
         }
-        if (g == 0) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                sm.m[warp][8 * n + 2 * j + x] = st.m[n][x];
-                sm.l[warp][8 * n + 2 * j + x] = st.l[n][x];
+        return false;
+    }
+};
+__device__ __forceinline__ int steps_of(const Tile &t) { return (t.t1 - t.t0 + kKeys - 1) / kKeys; }
+
+// ------------------------------------------------------------------ codes and scales of the steps
+// A step's keys and values arrive as one box per page part and 128 dimensions (zeros behind the
+// head).  Lanes 0 .. 7 look up a box's page, lanes 8 .. 15 a group's, and its scales, which go out
+// one step later, so that copies do not wait for them.
+template <int NB, int NR>
+__device__ __forceinline__ void copy_role(const KvAttnArgs &a, const CUtensorMap *km, const CUtensorMap *vm, Smem<NB, NR> &sm,
+                                          Share<NR> share)
+{
+    using S = Shape<NB, NR>;
+    const int lane = threadIdx.x % 32;
+    const int box_rows = min(1 << a.page_shift, kKeys), boxes = kKeys / box_rows;
+    const int my_key = lane < kGroups ? lane * box_rows : (lane - kGroups) * 16;
+    const bool boxed = lane < boxes, grouped = lane >= kGroups && lane < 2 * kGroups;
+    uint32_t step = 0;
+    float ks = 0.f, vs = 0.f;
+    bool bad = false, pending = false, ok = true;
+    auto publish = [&]() {  // the scales of step - 1
+        if (!pending) return;
+        const int slot = (step - 1) % S::kStages;
+        const uint32_t dead = __ballot_sync(0xffffffffu, bad) >> kGroups;
+        const float top = __uint_as_float(warp_umax(__float_as_uint(fabsf(vs))));
+        if (grouped) {
+            sm.ks[slot][lane - kGroups] = ks;
+            sm.vs[slot][lane - kGroups] = vs;
+        }
+        if (lane == 0) {
+            sm.dead[slot] = dead;
+            sm.v_max[slot] = top;
+            if (dead) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.scales[slot]);
+        pending = false;
+    };
+    Tile t;
+    while (ok && share.next(t)) {
+        const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
+        auto entry_of = [&](int key) { return (boxed || grouped) && key < t.t1 ? __ldg(table + (key >> a.page_shift)) : 0; };
+        const int n = steps_of(t);
+        int entry = n ? entry_of(t.t0 + my_key) : 0;
+        for (int j = 0; j < n; ++j) {
+            const int key = t.t0 + j * kKeys + my_key, slot = step % S::kStages;
+            const uint32_t round = step / S::kStages;
+            const bool used = (boxed || grouped) && key < t.t1;
+            const int64_t page = used ? kv_page_ok(entry, a.num_pages) : -1;
+            const int z = page < 0 ? -1 : int(page) * a.kv_heads + t.head;
+            const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, boxed && z >= 0))) * uint32_t(box_rows * 128 * NB);
+            const int y = key & ((1 << a.page_shift) - 1);
+            if (round && !wait_warp(&sm.empty[slot], (round - 1) & 1, &sm.abort)) {
+                ok = false;
+                break;
             }
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], 2 * bytes);
+            __syncwarp();
+            if (boxed && z >= 0)
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    tma_load_3d(sm.k[slot][c] + lane * box_rows * 128, km, 128 * c, y, z, &sm.full[slot]);
+                    tma_load_3d(sm.v[slot][c] + lane * box_rows * 128, vm, 128 * c, y, z, &sm.full[slot]);
+                }
+            publish();
+            ks = grouped && z >= 0 ? __ldg(a.k_scale + z) : 0.f;
+            vs = grouped && z >= 0 ? __ldg(a.v_scale + z) : 0.f;
+            bad = grouped && used && z < 0;
+            pending = true;
+            ++step;
+            if (j + 1 < n) entry = entry_of(key + kKeys);
         }
     }
-    constexpr int kQuarter = DT / 4, kPairs = kQuarter / 2;
+    publish();
+    // nothing may land in shared memory after the block exits
+    for (uint32_t i = step > uint32_t(S::kStages) ? step - S::kStages : 0; i < step; ++i)
+        wait_warp(&sm.full[i % S::kStages], (i / S::kStages) & 1, &sm.abort, 20000000);
+}
+
+// ------------------------------------------------------------------ MMA issue (one thread)
+template <bool F8, int NB, int NR>
+__device__ __forceinline__ void mma_role(const KvAttnArgs &a, Smem<NB, NR> &sm, Share<NR> share, uint32_t tbase, uint64_t *fin)
+{
+    using S = Shape<NB, NR>;
+    const uint32_t kmajor = F8 ? tc::idesc_f8(kKeys, S::kN) : tc::idesc_i8(kKeys, S::kN);
+    const uint32_t iqk = kmajor, ipv = kmajor | tc::kIdescATransposed;
+    const uint64_t dk = tc::sdesc_sw128(smem_u32(sm.k)), dv = tc::sdesc_sw128(smem_u32(sm.v));
+    const uint64_t dq = tc::sdesc_sw128(smem_u32(sm.q)), dp = tc::sdesc_sw128(smem_u32(sm.p));
+    // the scores of a step: 32 dimensions an MMA
+    auto qk = [&](uint32_t step) {
+        const uint64_t k = dk + uint64_t((step % S::kStages) * (NB * S::kBox) >> 4);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+        for (int c = 0; c < NB; ++c)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 4; ++i)
+                mma_8bit<F8>(tbase + S::kSCol + (step & 1) * S::kN, k + uint64_t((c * S::kBox + i * 32) >> 4),
+                             dq + uint64_t((c * S::kN * 128 + i * 32) >> 4), iqk, c + i > 0);
+        tc::commit(&sm.s_full[step & 1]);
+    };
+    // the sums of a step: 32 keys an MMA; A is dimension-major: 128 bytes of dimensions a key, groups
+    // of 8 keys 1024 bytes apart
+    auto pv = [&](uint32_t step) {
+        const uint64_t v = dv + uint64_t((step % S::kStages) * (NB * S::kBox) >> 4);
+        const uint64_t p = dp + uint64_t((step & 1) * (S::kN * 128) >> 4);
 #pragma unroll
-            for (int i = 0; i < DT / 64; ++i)
+        for (int c = 0; c < NB; ++c)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    *reinterpret_cast<float2 *>(&sm.o[warp][8 * n + 2 * j + x][16 * i + 2 * g]) =
-                        make_float2(st.o[n][h * (DT / 64) + i][x], st.o[n][h * (DT / 64) + i][2 + x]);
-        __syncthreads();
-        if (h == 0) {
-            if (tid < S::kRows) {
-                float m = -INFINITY, l = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][tid]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = weight_of(sm.m[w][tid], m);
-                    sm.f[w][tid] = f;
-                    l += f * sm.l[w][tid];
-                }
-                sm.top[tid] = m;
-                sm.weight[tid] = l;
-                if (slot && tid < t.rows) *reinterpret_cast<float2 *>(slot + tid * S::kRowFloats + DT) = make_float2(m, l);
-            }
-            __syncthreads();
+            for (int i = 0; i < 4; ++i)
+                mma_8bit<F8>(tbase + S::kOCol + ((step & 1) * NB + c) * S::kN, v + uint64_t((c * S::kBox + i * 4096) >> 4),
+                             p + uint64_t((i * 32) >> 4), ipv, i > 0);
+        tc::commit(&sm.o_full[step & 1]);
+        tc::commit(&sm.empty[step % S::kStages]);
+    };
+    uint32_t step = 0, queries = 0;
+    Tile t;
+    bool ok = true;
+    auto scores_of = [&](uint32_t s) {
+        if (!wait(&sm.full[s % S::kStages], (s / S::kStages) & 1, &sm.abort)) return false;
+        tc::fence_after_sync();
+        qk(s);
+        return true;
+    };
+    while (ok && share.next(t)) {
+        const int n = steps_of(t);
+        if (n == 0) continue;
+        ok = wait(&sm.q_full, queries++ & 1, &sm.abort) && scores_of(step);
+        for (int j = 0; j < n && ok; ++j, ++step) {
+            ok = (j + 1 == n || scores_of(step + 1)) && wait(&sm.p_full[step & 1], (step >> 1) & 1, &sm.abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            pv(step);
         }
-        for (int e = tid; e < t.rows * kPairs; e += kThreads) {
-            const int r = e / kPairs, at = 2 * (e % kPairs), place = h * kQuarter + at;
-            float x = 0.f, y = 0.f;
+    }
+    tc::commit(fin);  // all MMAs complete before the Tensor Memory is freed
+    wait(fin, 0, &sm.abort, 20000000);
+}
+
+// ------------------------------------------------------------------ softmax and output
+// Where the tile's rows are and what they see, by NR threads.
+template <int NB, int NR>
+__device__ __forceinline__ void place_rows(const KvAttnArgs &a, Smem<NB, NR> &sm, const Tile &t)
+{
+    const int r = threadIdx.x, row = t.row0 + r;
+    if (r >= NR) return;
+    const int i = r < t.rows ? row / a.group : 0, h = r < t.rows ? row % a.group : 0;
+    sm.row_at[r] = (int64_t(t.s.q0 + i) * a.q_heads + t.head * a.group + h) * a.head_dim;
+    sm.seen[r] = r < t.rows ? min(t.t1, t.s.len - t.s.n + i + 1) : 0;
+}
+
+// Rows [0, NR) of the tile to shared memory as parts, sixteen threads a row.
+template <bool F8, bool BF16, int NB, int NR>
+__device__ __forceinline__ void cut_queries(const KvAttnArgs &a, Smem<NB, NR> &sm, const Tile &t)
+{
+    using S = Shape<NB, NR>;
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    const int tid = threadIdx.x, x16 = tid % 16;
+#pragma unroll 1
+    for (int r = tid / 16; r < NR; r += kSoft / 16) {
+        const bool live = r < t.rows;
+        const uint16_t *q = static_cast<const uint16_t *>(a.q) + sm.row_at[r];
+        uint2 raw[NB][2];
+        uint32_t amax = 0;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 v = *reinterpret_cast<const float2 *>(&sm.o[w][r][at]);
-                x += sm.f[w][r] * v.x;
-                y += sm.f[w][r] * v.y;
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int d = 128 * c + 8 * x16 + 4 * h;
+                raw[c][h] = live && d < a.head_dim ? *reinterpret_cast<const uint2 *>(q + d) : make_uint2(0, 0);
+                const float2 lo = act_f2<T>(raw[c][h].x), hi = act_f2<T>(raw[c][h].y);
+                // (as bit patterns: infinities and NaN are the largest)
+                amax = max(max(max(amax, __float_as_uint(fabsf(lo.x))), max(__float_as_uint(fabsf(lo.y)), __float_as_uint(fabsf(hi.x)))),
+                           __float_as_uint(fabsf(hi.y)));
             }
-            if (slot) {
-                *reinterpret_cast<float2 *>(slot + r * S::kRowFloats + place) = make_float2(x, y);
-            } else {
-                const float inv = inverse_of(sm.weight[r]);
-                const int d = dim_of<DT>(place);
-                if (d < a.head_dim) *reinterpret_cast<uint32_t *>(out_row(a, t, r) + d) = act_t2<T>(x * inv, y * inv);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = kv_clamp(int(amax >> 23) - 127, -90, 120);
+        const float up = __uint_as_float(uint32_t(127 + kQUp<F8> - e) << 23);
+        const float down = __uint_as_float(uint32_t(127 + e - kQUp<F8>) << 23);
+        if (x16 == 0) sm.q_scale[r] = amax < 0x7f800000u ? down * (a.sm_scale * kLog2e) : __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            uint32_t part[2][kParts];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 lo = act_f2<T>(raw[c][h].x), hi = act_f2<T>(raw[c][h].y);
+                const float x[4] = {lo.x * up, lo.y * up, hi.x * up, hi.y * up};
+                split4<F8>(x, part[h]);
+            }
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const int n = p * NR + r;
+                *reinterpret_cast<uint2 *>(sm.q[c] + n * 128 + (((x16 / 2) ^ (n & 7)) << 4) + 8 * (x16 % 2)) =
+                    make_uint2(part[0][p], part[1][p]);
             }
         }
-        __syncthreads();
     }
 }
 
-// Joins the partials of a tile: those of `parts` blocks from p0 on (its second slot, the others'
-// first), in the order of their keys.
-template <typename T, int DT, int NT>
-__device__ __forceinline__ void join_parts(const KvAttnArgs &a, const Tile &t, const float *p0, int parts)
+// The block's part of a tile: scores, weights and sums step by step; `step` counts over all tiles.
+template <int NB, int NR>
+struct State {
+    float o[NB][NR];  // of the thread's dimension(s), over vref
+    float m[NR], l[NR], vref;  // l: of the thread's keys
+};
+
+template <bool F8, int NB, int NR>
+__device__ __forceinline__ void add_sums(Smem<NB, NR> &sm, uint32_t step, uint32_t tlane, const float (&f)[NR], State<NB, NR> &st)
 {
-    using S = Shape<DT, NT>;
-    constexpr int kQuads = DT / 4, kSlot = S::kRows * S::kRowFloats;
-    constexpr int kBatch = 8;  // parts whose loads are in flight together
-#pragma unroll 1
-    for (int e = threadIdx.x; e < t.rows * kQuads; e += kThreads) {
-        const int r = e / kQuads, place = 4 * (e % kQuads);
-        float m = -INFINITY, l = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int c0 = 0; c0 < parts; c0 += kBatch) {
-            float2 ml[kBatch];
-            float4 v[kBatch];
+    using S = Shape<NB, NR>;
+    wait_warp(&sm.o_full[step & 1], (step >> 1) & 1, &sm.abort);
+    tc::fence_after_sync();
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int c = min(c0 + i, parts - 1);
-                const float *row = p0 + c * (2 * kSlot) + (c == 0 ? kSlot : 0) + r * S::kRowFloats;
-                ml[i] = __ldcg(reinterpret_cast<const float2 *>(row + DT));
-                v[i] = __ldcg(reinterpret_cast<const float4 *>(row + place));
-            }
+    for (int c = 0; c < NB; ++c)
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (c0 + i >= parts) break;
-                const float top = fmaxf(m, ml[i].x), f = weight_of(m, top), w = weight_of(ml[i].x, top);
-                l = f * l + w * ml[i].y;
-                x.x = f * x.x + w * v[i].x;
-                x.y = f * x.y + w * v[i].y;
-                x.z = f * x.z + w * v[i].z;
-                x.w = f * x.w + w * v[i].w;
-                m = top;
+        for (int h = 0; h < NR / 8; ++h) {
+            uint32_t x[kParts][8];
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+                tc::ld_32x32b_x8(tlane + S::kOCol + ((step & 1) * NB + c) * S::kN + p * NR + 8 * h, x[p]);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 8 * h + i;
+                st.o[c][r] = fmaf(whole_of<F8>(x[0][i], x[1][i], x[2][i], x[3][i]), 1.f / kPUp<F8>, st.o[c][r] * f[r]);
             }
         }
-        uint16_t *out = out_row(a, t, r);
-        const float inv = inverse_of(l);
-        const int d0 = dim_of<DT>(place), d1 = dim_of<DT>(place + 2);
-        if (d0 < a.head_dim) *reinterpret_cast<uint32_t *>(out + d0) = act_t2<T>(x.x * inv, x.y * inv);
-        if (d1 < a.head_dim) *reinterpret_cast<uint32_t *>(out + d1) = act_t2<T>(x.z * inv, x.w * inv);
+}
+
+template <bool F8, int NB, int NR>
+__device__ __forceinline__ void attend(const KvAttnArgs &a, Smem<NB, NR> &sm, const Tile &t, uint32_t &step, uint32_t tbase,
+                                       State<NB, NR> &st)
+{
+    using S = Shape<NB, NR>;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, n = steps_of(t);
+    const uint32_t tlane = tbase + (uint32_t(32 * warp) << 16);
+    const int least = sm.seen[0];  // keys that every row sees
+    float f[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) f[r] = 1.f;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j, ++step) {
+        const int slot = step % S::kStages, b = step & 1, key0 = t.t0 + j * kKeys, key = key0 + tid;
+        wait_warp(&sm.scales[slot], (step / S::kStages) & 1, &sm.abort);
+        wait_warp(&sm.s_full[b], (step >> 1) & 1, &sm.abort);
+        tc::fence_after_sync();
+        const uint32_t dead = sm.dead[slot];
+        const bool gone = key >= t.t1 || (dead >> (tid / 16) & 1);
+        const bool masked = key0 + kKeys > least || dead;
+        const float ks = sm.ks[slot][tid / 16];
+        float s[NR];
+#pragma unroll
+        for (int h = 0; h < NR / 8; ++h) {
+            uint32_t x[kParts][8];
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) tc::ld_32x32b_x8(tlane + S::kSCol + b * S::kN + p * NR + 8 * h, x[p]);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 8 * h + i;
+                s[r] = whole_of<F8>(x[0][i], x[1][i], x[2][i], x[3][i]) * (ks * sm.q_scale[r]);
+            }
+        }
+        if (masked)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if (gone || key >= sm.seen[r]) s[r] = -INFINITY;
+        // ---- new references where a score rose too far over the maximum so far (or is the first), or
+        // a larger value scale arrived
+        float f_now[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) f_now[r] = 1.f;
+        const float vmax = sm.v_max[slot];
+        bool rose = vmax >= st.vref && vmax > 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) rose |= !(s[r] <= st.m[r] + kSlack);  // (NaN too)
+        if (soft_any(rose)) {
+            int mine = 0;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const int top = __reduce_max_sync(0xffffffffu, order_of(s[r]));
+                if (lane == r) mine = top;
+            }
+            if (lane < NR) sm.top[b][lane][warp] = mine;
+            named_bar_sync(1, kSoft);
+            float fv = 1.f;
+            if (vmax >= st.vref && vmax > 0.f) {
+                const float vnew = __uint_as_float((__float_as_uint(fmaxf(vmax, 0x1p-120f)) & 0x7f800000u) + 0x00800000u);
+                fv = st.vref * inverse_pow2(vnew);
+                st.vref = vnew;
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const int4 x = *reinterpret_cast<const int4 *>(sm.top[b][r]);
+                const float m = of_order(max(max(max(x.x, x.y), max(x.z, x.w)), order_of(st.m[r])));
+                const float fm = m == st.m[r] ? 1.f : exp2_approx(st.m[r] - m);
+                st.m[r] = m;
+                st.l[r] *= fm;
+                f_now[r] = fm * fv;
+            }
+        }
+        const float v = gone || st.vref == 0.f ? 0.f : sm.vs[slot][tid / 16] * (inverse_pow2(st.vref) * kPUp<F8>);
+        float w[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            w[r] = s[r] == -INFINITY ? 0.f : exp2_approx(s[r] - st.m[r]);
+            st.l[r] += w[r];
+        }
+        // ---- the weights' parts: a byte per (part, row), this thread's key
+        uint8_t *pb = sm.p[b];
+#pragma unroll
+        for (int r0 = 0; r0 < NR; r0 += 4) {
+            const float x[4] = {w[r0] * v, w[r0 + 1] * v, w[r0 + 2] * v, w[r0 + 3] * v};
+            uint32_t part[kParts];
+            split4<F8>(x, part);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = p * NR + r0 + i;
+                    pb[row * 128 + (((tid / 16) ^ (row & 7)) << 4) + tid % 16] = uint8_t(part[p] >> (8 * i));
+                }
+        }
+        if (F8 && gone) {  // slots without a key may hold NaN codes, which a weight of 0 does not silence
+#pragma unroll 1
+            for (int c = 0; c < NB * 8; ++c) sts128(sm.v[slot][c / 8] + tid * 128 + c % 8 * 16, make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[b]);
+        // ---- the sums of the step before, while this one's are on their way
+        if (j > 0) add_sums<F8, NB, NR>(sm, step - 1, tlane, f, st);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) f[r] = f_now[r];
+    }
+    if (n) add_sums<F8, NB, NR>(sm, step - 1, tlane, f, st);
+}
+
+// The finished rows of a tile, or this block's partial in `slot`.
+template <typename T, int NB, int NR>
+__device__ __forceinline__ void finish(const KvAttnArgs &a, Smem<NB, NR> &sm, const Tile &t, State<NB, NR> &st, float *slot)
+{
+    using S = Shape<NB, NR>;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    float mine = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        float l = st.l[r];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == r) mine = l;
+    }
+    if (lane < NR) sm.sum[warp][lane] = mine;
+    named_bar_sync(1, kSoft);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        if (r >= t.rows) break;
+        const float l = sm.sum[0][r] + sm.sum[1][r] + sm.sum[2][r] + sm.sum[3][r];
+        const float scale = slot ? st.vref : st.vref * inverse_of(l);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            const int d = 128 * c + tid;
+            const float x = st.vref > 0.f ? st.o[c][r] * scale : (l == l ? 0.f : l);
+            if (slot) slot[r * S::kRowFloats + d] = x;
+            else if (d < a.head_dim) static_cast<T *>(a.out)[sm.row_at[r] + d] = act_t<T>(x);
+        }
+        if (slot && tid == 0) *reinterpret_cast<float2 *>(slot + r * S::kRowFloats + 128 * NB) = make_float2(st.m[r], l);
+    }
+    named_bar_sync(1, kSoft);  // the sums are read
+}
+
+// Joins the partials of a tile: those of `parts` blocks from p0 on (its second slot, the others'
+// first), in the order of their keys.  They come to the ring's memory in one go; `round` counts the
+// waits on sm.joined.
+template <typename T, int NB, int NR>
+__device__ __forceinline__ void join_parts(const KvAttnArgs &a, Smem<NB, NR> &sm, const Tile &t, const float *p0, int parts,
+                                           uint32_t &round)
+{
+    using S = Shape<NB, NR>;
+    constexpr int kQuads = 32 * NB, kSlot = NR * S::kRowFloats, kPer = (kQuads * NR + kSoft - 1) / kSoft;
+    constexpr int kChunk = 2 * S::kStages * NB * S::kBox / (4 * kSlot) < kSoft ? 2 * S::kStages * NB * S::kBox / (4 * kSlot) : kSoft;
+    const int tid = threadIdx.x;
+    float *ring = reinterpret_cast<float *>(&sm.k);
+    float m[kPer], l[kPer];
+    float4 x[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < parts; c0 += kChunk) {
+        const int n = min(kChunk, parts - c0);
+        fence_proxy_async();         // what the block wrote and read there before
+        fence_proxy_async_global();  // the partials, written with plain stores
+        named_bar_sync(1, kSoft);
+        if (tid == 0) mbar_arrive_expect_tx(&sm.joined, uint32_t(n * kSlot * 4));
+        named_bar_sync(1, kSoft);
+        if (tid < n) {
+            const int c = c0 + tid;
+            bulk_load(ring + tid * kSlot, p0 + int64_t(c) * (2 * kSlot) + (c == 0 ? kSlot : 0), uint32_t(kSlot * 4), &sm.joined);
+        }
+        wait_warp(&sm.joined, round++ & 1, &sm.abort, 20000000);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int e = tid + k * kSoft, r = e / kQuads, d = 4 * (e % kQuads);
+            if (r >= t.rows) break;
+#pragma unroll 4
+            for (int c = 0; c < n; ++c) {
+                const float *row = ring + c * kSlot + r * S::kRowFloats;
+                const float2 ml = *reinterpret_cast<const float2 *>(row + 128 * NB);
+                const float4 v = *reinterpret_cast<const float4 *>(row + d);
+                const float top = of_order(max(order_of(m[k]), order_of(ml.x)));
+                const float f = weight_of(m[k], top), w = weight_of(ml.x, top);
+                l[k] = f * l[k] + w * ml.y;
+                x[k].x = f * x[k].x + w * v.x;
+                x[k].y = f * x[k].y + w * v.y;
+                x[k].z = f * x[k].z + w * v.z;
+                x[k].w = f * x[k].w + w * v.w;
+                m[k] = top;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int e = tid + k * kSoft, r = e / kQuads, d = 4 * (e % kQuads);
+        if (r >= t.rows || d >= a.head_dim) continue;
+        const float inv = inverse_of(l[k]);
+        *reinterpret_cast<uint2 *>(out_row(a, t, r) + d) =
+            make_uint2(act_t2<T>(x[k].x * inv, x[k].y * inv), act_t2<T>(x[k].z * inv, x[k].w * inv));
     }
 }
 
@@ -684,23 +725,114 @@ __device__ __forceinline__ int share_of(int total, int c, int grid)
     return int(q * unsigned(c) + r * unsigned(c) / unsigned(grid));
 }
 
-template <bool F8, bool BF16, int DT, int NT>
+template <bool F8, bool BF16, int NB, int NR>
+__device__ __forceinline__ void soft_role(const KvAttnArgs &a, Smem<NB, NR> &sm, Share<NR> share, uint32_t tbase, int total,
+                                          int grid)
+{
+    using S = Shape<NB, NR>;
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    constexpr int kSlot = NR * S::kRowFloats;
+    const int tid = threadIdx.x, lane = tid % 32, cta = blockIdx.x, u_end = share.u_end;
+    Tile t, kept[2];
+    bool kept_any[2] = {false, false};  // partials of a tile that began before, of one that ends behind
+    uint32_t step = 0;
+#pragma unroll 1
+    while (share.next(t)) {
+        place_rows<NB, NR>(a, sm, t);
+        named_bar_sync(1, kSoft);
+        if (steps_of(t)) {
+            cut_queries<F8, BF16, NB, NR>(a, sm, t);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full);
+            named_bar_sync(1, kSoft);  // the rows' scales are written
+        }
+        State<NB, NR> st;
+        st.vref = 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            st.m[r] = -INFINITY;
+            st.l[r] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NB; ++c) st.o[c][r] = 0.f;
+        }
+        attend<F8, NB, NR>(a, sm, t, step, tbase, st);
+        finish<T, NB, NR>(a, sm, t, st, t.whole ? nullptr : a.partials + int64_t(2 * cta + (t.first ? 1 : 0)) * kSlot);
+        if (!t.whole) {
+            if (t.first) kept[1] = t;
+            else kept[0] = t;
+            kept_any[t.first] = true;
+        }
+    }
+    // Every partial of the block is written: it arrives at the counters of their tiles (of the
+    // tile's first block), and joins the parts of those that it is the last to arrive at.
+    if (!kept_any[0] && !kept_any[1]) return;
+    if (tid == 0) {
+        auto owner = [&](int x) {
+            int c = min(grid - 1, int(float(x) * (float(grid) / float(total))));  // near the block that holds unit x
+            while (c > 0 && share_of(total, c, grid) > x) --c;
+            while (share_of(total, c + 1, grid) <= x) ++c;
+            return c;
+        };
+        int c0[2], parts[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (kept_any[i]) {
+                c0[i] = i ? cta : owner(kept[i].u0);
+                parts[i] = (kept[i].u1 - 1 < u_end ? cta : owner(kept[i].u1 - 1)) - c0[i] + 1;
+            }
+        fence_gpu();  // the block's partials, seen by this thread at the barrier, before its arrivals
+        bool last[2] = {false, false};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (kept_any[i]) last[i] = atomicInc(&a.arrivals[c0[i]], unsigned(parts[i] - 1)) == unsigned(parts[i] - 1);
+        if (last[0] || last[1]) fence_gpu();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sm.first[i] = last[i] ? c0[i] : 0;
+            sm.parts[i] = last[i] ? parts[i] : 0;
+        }
+    }
+    named_bar_sync(1, kSoft);
+    uint32_t round = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+        if (kept_any[i] && sm.parts[i])
+            join_parts<T, NB, NR>(a, sm, i ? kept[1] : kept[0], a.partials + int64_t(sm.first[i]) * (2 * kSlot), sm.parts[i], round);
+}
+
+template <bool F8, bool BF16, int NB, int NR>
 __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtensorMap &vm, const KvAttnArgs &a)
 {
-    using S = Shape<DT, NT>;
+    using S = Shape<NB, NR>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Smem<DT, NT> &sm = *reinterpret_cast<Smem<DT, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t fin;
+    Smem<NB, NR> &sm = *reinterpret_cast<Smem<NB, NR> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int *before = reinterpret_cast<int *>(&sm + 1);  // units of sequences < b
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
-        for (int w = 0; w < kWarps; ++w)
-            for (int i = 0; i < S::kBufs; ++i) mbar_init(&sm.full[w][i], 1);
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.scales[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], kSoft / 32);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        mbar_init(&sm.q_full, kSoft / 32);
+        mbar_init(&sm.joined, 1);
+        mbar_init(&fin, 1);
         sm.abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&km);
         tma_prefetch_desc(&vm);
     }
-    grid_dep_launch();
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&sm.tmem, S::kTmem);
+        tc::tmem_relinquish();
+    }
     if (!a.behind_tiles) grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
 
     // units of every sequence, summed up: each thread takes a run of sequences
@@ -712,7 +844,8 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
         const KvSpan s = kv_span(a.cu_q[b], a.cu_q[b + 1], len, a.M, a.capacity);
         if (len > a.capacity) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
         if (int64_t(s.n) * a.group > a.few_rows) return int64_t(0);
-        return kv_tiles(s.n, a.group, S::kRows) * a.kv_heads * (split ? kTileUnits + kv_units(s.len, 1 << shift) : 1);
+        const int64_t units = max(int64_t(1), (int64_t(s.len) + (1 << shift) - 1) >> shift);  // kv_units
+        return kv_tiles(s.n, a.group, NR) * a.kv_heads * (split ? kTileUnits + units : 1);
     };
     int64_t mine, sum, all;
     for (;; ++shift) {  // (larger units where their count would not fit: more than 2^36 keys)
@@ -725,13 +858,13 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
             const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += x;
         }
-        if (lane == 31) sm.sums[warp] = sum;
+        if (lane == 31) sm.units[warp] = sum;
         __syncthreads();
         all = 0;
         int64_t below = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) below += sm.sums[w];
-            all += sm.sums[w];
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) below += sm.units[w];
+            all += sm.units[w];
         }
         sum += below - mine;
         if (all <= kMostUnits || shift == 30) break;
@@ -746,120 +879,66 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
         }
     }
     if (tid == 0) before[a.n_seqs] = total;
-    __syncthreads();
-
     // no more shares than units, so that no block between a tile's first and last is without one
     const int least = split ? kTileUnits + kLeastUnits : 1;
     const int grid = min(int(gridDim.x), (total + least - 1) / least), cta = blockIdx.x;
-    if (cta >= grid) return;
-    int u = share_of(total, cta, grid);
-    const int u_end = share_of(total, cta + 1, grid);
-    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-    constexpr int kSlot = S::kRows * S::kRowFloats;
-    // the block's next part of a tile (u: the unit behind it)
-    auto next_part = [&](Tile &t) {
-        while (u < u_end) {
-            int next;
-            t = tile_of<S::kRows>(a, before, shift, u, u_end, next);
-            u = next;
-            if (next > t.u0) return true;  // (else none of the tile's keys)
-        }
-        return false;
-    };
-    Walk<DT, NT> walk(a, &km, &vm, sm);
-    Tile t, ahead, kept[2];
-    bool kept_any[2] = {false, false};  // partials of a tile that began before, of one that ends behind
-    bool more = next_part(t);
-    if (more) walk.begin(t);
-#pragma unroll 1
-    while (more) {
-        State<DT, NT> st;
-        walk.template run<F8, BF16>(st);
-        more = next_part(ahead);
-        if (more) walk.begin(ahead);
-        float *slot = t.whole ? nullptr : a.partials + int64_t(2 * cta + (t.first ? 1 : 0)) * kSlot;
-        join<T, DT, NT>(a, sm, t, st, slot);
-        if (!t.whole) {
-            if (t.first) kept[1] = t;
-            else kept[0] = t;
-            kept_any[t.first] = true;
-        }
-        t = ahead;
-    }
-    // Every partial of the block is written: it arrives at the counters of their tiles (of the
-    // tile's first block), and joins the parts of those that it is the last to arrive at.
-    if (!kept_any[0] && !kept_any[1]) return;
-    if (tid == 0) {
-        auto owner = [&](int x) {
-            int c = int(unsigned(int64_t(x) * grid / total));  // at or next to the block that holds unit x
-            while (c > 0 && share_of(total, c, grid) > x) --c;
-            while (share_of(total, c + 1, grid) <= x) ++c;
-            return c;
-        };
-        int c0[2], parts[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (kept_any[i]) {
-                c0[i] = i ? cta : owner(kept[i].u0);
-                parts[i] = (i ? owner(kept[i].u1 - 1) : (kept[i].u1 - 1 < u_end ? cta : owner(kept[i].u1 - 1))) - c0[i] + 1;
-            }
-        fence_gpu();  // the block's partials, seen by this thread at the barrier, before its arrivals
-        bool last[2] = {false, false};
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (kept_any[i]) last[i] = atomicInc(&a.arrivals[c0[i]], unsigned(parts[i] - 1)) == unsigned(parts[i] - 1);
-        if (last[0] || last[1]) fence_gpu();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            sm.first[i] = last[i] ? c0[i] : 0;
-            sm.parts[i] = last[i] ? parts[i] : 0;
-        }
-    }
+    tc::fence_before_sync();
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (kept_any[i] && sm.parts[i])
-            join_parts<T, DT, NT>(a, kept[i], a.partials + int64_t(sm.first[i]) * (2 * kSlot), sm.parts[i]);
+    tc::fence_after_sync();
+    grid_dep_launch();  // (after the Tensor Memory is taken: the next kernel may want all of it)
+    const uint32_t tbase = sm.tmem;
+    if (cta >= grid) {
+        if (warp == kMmaWarp) tc::tmem_dealloc(tbase, S::kTmem);
+        return;
+    }
+    const Share<NR> share{a, before, shift, share_of(total, cta, grid), share_of(total, cta + 1, grid)};
+    if (warp < kSoft / 32) {
+        soft_role<F8, BF16, NB, NR>(a, sm, share, tbase, total, grid);
+    } else if (warp == kCopyWarp) {
+        copy_role<NB, NR>(a, &km, &vm, sm, share);
+    } else if (lane == 0) {
+        mma_role<F8, NB, NR>(a, sm, share, tbase, &fin);
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tbase, S::kTmem);
 }
 
-template <bool F8, bool BF16, int DT, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<DT, NT>::kPerSm)
+template <bool F8, bool BF16, int NB, int NR>
+__global__ void __launch_bounds__(kThreads, Shape<NB, NR>::kPerSm)
 kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                     const __grid_constant__ KvAttnArgs a)
 {
-    attend_rows<F8, BF16, DT, NT>(km, vm, a);
+    attend_rows<F8, BF16, NB, NR>(km, vm, a);
     if (a.behind_tiles) grid_dep_wait();
 }
 
 struct RowsPlan {
     const void *fn;
     int per_sm;
-    size_t smem;    // without the unit counts
-    int row_bytes;  // of a copied box
-    int keys;       // of a stage
+    size_t smem;  // without the unit counts
 };
 
-template <bool F8, bool BF16, int DT, int NT>
+template <bool F8, bool BF16, int NB, int NR>
 RowsPlan rows_plan()
 {
-    using S = Shape<DT, NT>;
-    return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, DT, NT>), S::kPerSm,
-            sizeof(Smem<DT, NT>) + 1024, S::kRowBytes, S::kKeys};
+    return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, NB, NR>), Shape<NB, NR>::kPerSm, sizeof(Smem<NB, NR>) + 1024};
 }
 
 template <bool F8, bool BF16>
 RowsPlan rows_plan(int head_dim, bool two)
 {
-    if (head_dim <= 64) return two ? rows_plan<F8, BF16, 64, 2>() : rows_plan<F8, BF16, 64, 1>();
-    if (head_dim <= 128) return two ? rows_plan<F8, BF16, 128, 2>() : rows_plan<F8, BF16, 128, 1>();
-    return two ? rows_plan<F8, BF16, 256, 2>() : rows_plan<F8, BF16, 256, 1>();
+    if (head_dim <= 128) return two ? rows_plan<F8, BF16, 1, 16>() : rows_plan<F8, BF16, 1, 8>();
+    return two ? rows_plan<F8, BF16, 2, 16>() : rows_plan<F8, BF16, 2, 8>();
 }
 
 constexpr int kMostPerSm = 2;
 constexpr int kFewRows = 16;
-// two partial slots a block in the workspace's 64 KB per SM: two blocks of 8 rows of 132 binary32
+// two partial slots a block in the workspace's 64 KB per SM: two blocks of 16 rows of 132 binary32
 // values, or one of 16 rows of 260
-static_assert(2 * 2 * 8 * (128 + 4) * 4 <= 65536 && 2 * 16 * (256 + 4) * 4 <= 65536, "");
+static_assert(2 * 2 * 16 * (128 + 4) * 4 <= 65536 && 2 * 16 * (256 + 4) * 4 <= 65536, "");
 
 }  // namespace
 
@@ -905,7 +984,7 @@ wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
     if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem + (kKvMaxSeqs + 1) * sizeof(int))) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_rows_kernel)");
     CUtensorMap km, vm;
-    wq_status rc = encode_cache(&km, &vm, a, p.row_bytes, std::min(1 << a.page_shift, p.keys));
+    wq_status rc = encode_cache(&km, &vm, a, 128, std::min(1 << a.page_shift, kKeys));
     if (rc != WQ_OK) return rc;
     PreparedLaunch L;
     set_attn_launch(L, p.fn, unsigned(device_info().sm_count * p.per_sm), kThreads, smem, km, vm, a);

@@ -75,6 +75,14 @@ __device__ __forceinline__ void st_32x32b_x8(uint32_t taddr, const uint32_t (&v)
                  : "memory");
 }
 
+__device__ __forceinline__ void ld_32x32b_x8(uint32_t taddr, uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16])
 {
     asm volatile(
@@ -128,6 +136,27 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d_taddr, uint32_t a_taddr, ui
         : "memory");
 }
 
+// 8-bit operands, both in shared memory.
+__device__ __forceinline__ void mma_i8_ss(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_taddr),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // The mbarrier receives one arrival once all tcgen05 operations this thread issued before
 // have completed.
 __device__ __forceinline__ void commit(uint64_t *bar)
@@ -135,6 +164,10 @@ __device__ __forceinline__ void commit(uint64_t *bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
+
+// Added to an instruction descriptor: A is M-major (bit 15), in shared memory rows of M with the
+// 128-byte swizzle, groups of 8 k the stride byte offset apart.
+constexpr uint32_t kIdescATransposed = 1u << 15;
 
 // Instruction descriptor of kind::f16 with fp32 accumulation, both operands K-major:
 // D format (bits 4-5) = F32, A / B format (bits 7-9 / 10-12) = F16 (0) or BF16 (1),

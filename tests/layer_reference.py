@@ -141,14 +141,14 @@ def append_bits(qkv, cache, cu_q, seq_len, table, q_heads, kv_heads, rope, style
 
 
 def attention_64(q, cache, cu_q, seq_len, table, sm_scale, num_pages):
-    """(out, mass, score, plain, top, own): the attention in 64 bits, and for every output the terms its
-    error bound is made of: sum w |v|, the largest error of a score in units of 2^-24, sum |v|, and
-    the sum of |codes| times the largest value scale.
+    """(out, mass, score, top, own): the attention in 64 bits, and for every output the terms its
+    error bound is made of: sum w |v|, the largest error of a score in units of 2^-24, and the sum of
+    |codes| times the largest value scale.
     own: the rows that belong to a sequence.  Tokens whose block-table entry is no page are left
     out."""
     M, Hq, D = q.shape
     Hkv, ps = cache.k.shape[1], cache.page
-    out, mass, plain, top, score = (np.zeros((M, Hq, d)) for d in (D, D, D, D, 1))
+    out, mass, top, score = (np.zeros((M, Hq, d)) for d in (D, D, D, 1))
     own = np.zeros(M, bool)
     for b in range(len(seq_len)):
         n, ln = cu_q[b + 1] - cu_q[b], seq_len[b]
@@ -175,9 +175,8 @@ def attention_64(q, cache, cu_q, seq_len, table, sm_scale, num_pages):
                 rows = (cu_q[b] + i, slice(h * G, (h + 1) * G))
                 out[rows] = w @ v[see]
                 mass[rows] = w @ np.abs(v[see])
-                plain[rows] = np.abs(v[see]).sum(0)
                 top[rows] = np.abs(vc[see]).sum(0) * vs[see].max()
                 # D products and sums; the queries' 16-bit form: 2^-25 of the largest, per term
                 err = (D + 16) * (np.abs(qs) @ np.abs(k[see]).T) + np.abs(qs).max(1, keepdims=True) * np.abs(k[see]).sum(1)
                 score[rows] = (err * abs(sm_scale)).max(1, keepdims=True)
-    return out, mass, score, plain, top, own
+    return out, mass, score, top, own

@@ -319,16 +319,18 @@ def test_append_twice_is_the_same_as_once():
 
 
 # ---------------------------------------------------------------- attention
-def _bound(want, mass, score, plain, keys, dtype):
+def _bound(want, mass, score, top, keys, dtype):
     """The result's own rounding, and errors of the weighted sum: weights in binary16 (2^-11 of
     each), scores (in units of 2^-24; a weight moves by as much, numerator and denominator:
-    twice), the exponentials and rescalings (2^-18), one sum per 16 keys (2^-24 each).  Weights
-    enter binary16 as 2^15 times their share of the largest one; below 2^-14 binary16 has steps of
-    2^-24, half a step is 2^-25, so a weight is also off by up to 2^-25 / 2^15 = 2^-40 of the
-    largest, which is at most 1: 2^-40 sum |v|."""
+    twice), the exponentials and rescalings (2^-18), one sum per 16 keys (2^-24 each).  A weight is
+    also off by an absolute amount.  Few rows: weights of at most 1 times their value scale over a
+    power of two that is at most twice the largest scale are cut to multiples of 2^-28 (INT8
+    digits; e4m3 parts: subnormal steps of 2^-9 / (256 * 16^3) = 2^-29), half a step is 2^-29,
+    times 2: 2^-28 of the largest scale, for every code.  Many rows: binary16 of 2^11 times the
+    same, half a subnormal step of 2^-25: 2^-25 / 2^11 * 2 = 2^-35."""
     rel = 2.0 ** -11 + 2 * 2.0 ** -24 * score + 2.0 ** -18 + (keys / 16 + 32) * 2.0 ** -24
     tiny = 2.0 ** -25 if dtype == "fp16" else 0.0  # binary16 subnormals
-    return U[dtype] * np.abs(want) * 1.01 + rel * mass * 1.01 + 2.0 ** -40 * plain + tiny
+    return U[dtype] * np.abs(want) * 1.01 + rel * mass * 1.01 + 2.0 ** -28 * top + tiny
 
 
 def _attend(s, q, cache, batch, workspace=True, **kw):
@@ -337,19 +339,13 @@ def _attend(s, q, cache, batch, workspace=True, **kw):
     return wq.kv_attention(_dev(q, s.dt), cache, batch, out=out, workspace=ws, **kw)
 
 
-def _attend_check(s, q, got, sm_scale=None, tiles=False):
+def _attend_check(s, q, got, sm_scale=None):
     sm = s.D ** -0.5 if sm_scale is None else sm_scale
-    want, mass, score, plain, top, own = ref.attention_64(q, s.host, s.cu, s.total, s.table, float(np.float32(sm)), s.num_pages)
+    want, mass, score, top, own = ref.attention_64(q, s.host, s.cu, s.total, s.table, float(np.float32(sm)), s.num_pages)
     g = _np(got)
     assert (g[~own] == MARK).all()
     off = np.abs(g - want)[own]
-    lim = _bound(want, mass, score, plain, max(s.total), s.dtype)
-    if tiles:
-        # many rows: a weight enters binary16 as 2^11 times its share of a reference that is at most
-        # the largest weight, times its value scale over a power of two that is at most twice the
-        # largest: half a step, 2^-25, is 2^-25 / 2^11 * 2 = 2^-35 of the largest scale
-        lim = lim + 2.0 ** -35 * top
-    lim = lim[own]
+    lim = _bound(want, mass, score, top, max(s.total), s.dtype)[own]
     assert np.isfinite(g[own]).all()
     assert (off <= lim).all(), f"worst {np.max(off / np.maximum(lim, 1e-300))} of the bound"
 
@@ -440,7 +436,7 @@ def test_attention_many_rows(case, dtype, out):
     cache, batch = s.device()
     q = s.q()
     got = _attend(s, q, cache, batch)
-    _attend_check(s, q, got, tiles=True)
+    _attend_check(s, q, got)
     assert torch.equal(_attend(s, q, cache, batch), got)
 
 
@@ -455,7 +451,7 @@ def test_attention_many_rows_uneven(out):
     s.host.ks[order, 0] = (s.host.ks[order, 0] * 10.0 ** np.linspace(-2, 0.8, order.size)).astype(np.float32)
     q = s.q()
     cache, batch = s.device()
-    _attend_check(s, q, _attend(s, q, cache, batch), tiles=True)
+    _attend_check(s, q, _attend(s, q, cache, batch))
 
 
 def test_attention_many_rows_with_a_bad_page():
@@ -466,7 +462,7 @@ def test_attention_many_rows_with_a_bad_page():
     got = _attend(s, q, cache, batch)
     torch.cuda.synchronize()
     assert wq.device_error() == 3
-    _attend_check(s, q, got, tiles=True)
+    _attend_check(s, q, got)
 
 
 def test_attention_many_sequences():
