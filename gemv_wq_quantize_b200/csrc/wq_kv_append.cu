@@ -7,8 +7,9 @@
 // tokens by (scale before / scale).
 //
 // Work items.  The maximum over a page's new tokens needs one owner per (page, head): a block
-// owns one (sequence, page) item and a few heads.  Which sequence an item belongs to follows
-// from cu_q alone (wq_kv.h), found by all threads of the block looking at once.  A group of WPT
+// owns one (sequence, page) item and a head's keys or values; which sequence an item belongs to
+// follows from cu_q alone (wq_kv.h), found by all threads of the block looking at once.  Where
+// sequences bring few tokens, a block owns a sequence and four heads, a warp for each.  A group of WPT
 // warps owns the keys or the values of one head: every lane holds four neighbouring values of a
 // row (so the partner of a rotated value is one more 8-byte load of the same row, not a
 // shuffle), the rows of the page go over the group's warps, and the rotated values stay in
@@ -43,9 +44,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kHeldFloats = 32;  // binary32 values of a page that a lane keeps in registers
 
 // How the values of a row turn: kPairs: partners among a lane's four values, cos / sin in aligned
-// pairs; kHalf: partners rope_dim / 2 away, everything 8-byte aligned; kAny: neither (a rope_dim
-// that is no multiple of 4 or 8); kNone.
-enum Mode { kNone, kPairs, kHalf, kAny };
+// pairs; kHalf: partners rope_dim / 2 away, everything 8-byte aligned (rope_dim a multiple of 8);
+// kHalf2: the same with 4-byte alignment (a multiple of 4); kAny: the rest; kNone.
+enum Mode { kNone, kPairs, kHalf, kHalf2, kAny };
 
 struct AppendArgs {
     const void *qkv;
@@ -59,7 +60,7 @@ struct AppendArgs {
     int capacity;       // tokens that the block table's row holds
     int limit;          // positions below it have a place: min(capacity, rope_len)
     bool pairs;         // WQ_ROPE_PAIRS
-    int64_t kv_items;   // (sequence, page) items
+    int64_t kv_items;   // (sequence, page) items, or sequences (few tokens each)
     int parts;          // blocks per item
     int q_tokens;       // tokens of a query block
 };
@@ -72,7 +73,7 @@ struct Turn {
     float c[4], s[4];
 };
 struct Raw {
-    uint2 x, p;  // the values and (kHalf) their partners
+    uint2 x, p;  // the values and (but for kPairs) their partners
 };
 
 template <Mode MODE>
@@ -94,6 +95,17 @@ __device__ __forceinline__ Turn load_turn(const AppendArgs &a, const float *tab,
         const float4 s = __ldg(reinterpret_cast<const float4 *>(tab + half + u));
         t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
         t.s[0] = s.x; t.s[1] = s.y; t.s[2] = s.z; t.s[3] = s.w;
+    } else if constexpr (MODE == kHalf2) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const int e = min(d + i, a.rope_dim - 2), u = e < half ? e : e - half;
+            const float2 c = __ldg(reinterpret_cast<const float2 *>(tab + u));
+            const float2 s = __ldg(reinterpret_cast<const float2 *>(tab + half + u));
+            t.c[i] = c.x;
+            t.c[i + 1] = c.y;
+            t.s[i] = s.x;
+            t.s[i + 1] = s.y;
+        }
     } else if constexpr (MODE == kAny) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -114,6 +126,15 @@ __device__ __forceinline__ Raw load_raw(const AppendArgs &a, const T *row, int d
     if constexpr (MODE == kHalf) {
         const int half = a.rope_dim / 2;
         r.p = __ldg(reinterpret_cast<const uint2 *>(row + (d < half ? d + half : (d < a.rope_dim ? d - half : d))));
+    } else if constexpr (MODE == kHalf2) {
+        const int half = a.rope_dim / 2;
+        uint32_t p[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = min(d + 2 * i, a.rope_dim - 2);
+            p[i] = __ldg(reinterpret_cast<const uint32_t *>(row + (e < half ? e + half : e - half)));
+        }
+        r.p = make_uint2(p[0], p[1]);
     } else if constexpr (MODE == kAny) {
         const uint16_t *w = reinterpret_cast<const uint16_t *>(row);
         const int half = a.rope_dim / 2;
@@ -135,7 +156,7 @@ __device__ __forceinline__ void turn4(const AppendArgs &a, int d, const Raw &r, 
     const float2 lo = act_f2<T>(r.x.x), hi = act_f2<T>(r.x.y);
     const float x[4] = {lo.x, lo.y, hi.x, hi.y};
     float p[4] = {x[1], x[0], x[3], x[2]};
-    if constexpr (MODE == kHalf || MODE == kAny) {
+    if constexpr (MODE == kHalf || MODE == kHalf2 || MODE == kAny) {
         const float2 plo = act_f2<T>(r.p.x), phi = act_f2<T>(r.p.y);
         p[0] = plo.x; p[1] = plo.y; p[2] = phi.x; p[3] = phi.y;
     }
@@ -181,11 +202,13 @@ __device__ __forceinline__ uint32_t store_codes(float (&y)[4], const CodeScale &
 // values of a head (a lane has four of each).  s_max: one value per warp.
 template <typename T, bool F8, int WPT, int CH, Mode MODE>
 __device__ __forceinline__ void append_rows(const AppendArgs &a, const T *src, const float *tab, const KvPageSpan &ps,
-                                            int count, bool live, int head, int64_t page, float *scale, uint8_t *codes,
-                                            int wi, float *s_max)
+                                            int count, bool live, float *scale, uint8_t *codes, int wi,
+                                            float *s_max)
 {
     constexpr int kHeld = kHeldFloats / (4 * CH);
-    constexpr int kBatch = kHeld < 4 ? kHeld : 4;  // rows whose loads are in flight together
+    // Rows whose loads are in flight together.  A warp that has a page to itself mostly holds one or
+    // two rows: more at once is code to step over (few tokens: 9.6 us with 4, 7.7 with 1).
+    constexpr int kBatch = WPT == 1 ? 1 : kHeld < 8 ? kHeld : 8;
     const int lane = threadIdx.x % 32, D = a.c.head_dim;
     const int64_t row_stride = int64_t(a.q_heads + 2 * a.c.kv_heads) * D;
     auto dim = [&](int c) { return 4 * (lane + 32 * c); };
@@ -282,36 +305,16 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, const T *src, c
         }
 }
 
-// Keys and values of one (sequence, page) item.
+// Keys and values of one page of a sequence.
 template <typename T, bool F8, int WPT, int CH, Mode MODE>
-__device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, int part)
+__device__ __forceinline__ void append_page(const AppendArgs &a, int b, int seq_len, const KvPageSpan &ps, int part, float *s_max)
 {
     constexpr int kTasks = kWarps / WPT;  // (head, keys or values) pairs of the block
-    __shared__ int s_seq[4];
-    __shared__ float s_max[kWarps];
     const int tid = threadIdx.x, warp = tid / 32;
-    if (tid == 0) s_seq[0] = -1;
-    __syncthreads();
-    for (int b = tid; b < a.n_seqs; b += kThreads) {
-        const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
-        const int q0 = kv_clamp(lo, 0, a.M), q1 = kv_clamp(hi, q0, a.M);
-        if (kv_item_start(q0, b, a.page_shift) <= item && item < kv_item_start(q1, b + 1, a.page_shift)) {
-            s_seq[0] = b;
-            s_seq[1] = lo;
-            s_seq[2] = hi;
-            s_seq[3] = len;
-        }
-    }
-    __syncthreads();
-    const int b = s_seq[0];
-    if (b < 0) return;
-    const KvSpan span = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
-    const KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift), a.page_shift);
-    if (ps.count == 0) return;
     const int pos0 = (ps.page << a.page_shift) + ps.off;
     const int count = min(ps.count, a.limit - pos0);  // positions beyond the rope table have no place
     const int64_t page = kv_page_ok(__ldg(a.block_table + int64_t(b) * a.max_pages + ps.page), a.c.num_pages);
-    if (tid == 0 && (page < 0 || count < ps.count || s_seq[3] > a.capacity))
+    if (tid == 0 && (page < 0 || count < ps.count || seq_len > a.capacity))
         atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
     if (page < 0 || count <= 0) return;
 
@@ -325,10 +328,47 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, i
     uint8_t *codes = static_cast<uint8_t *>(is_k ? a.c.k : a.c.v) +
                      kv_code_offset(page, head, 0, a.c.kv_heads, a.page_shift, a.pitch);
     if (MODE != kNone && is_k)  // (one answer for the warps of a task, and with WPT > 1 for the block)
-        append_rows<T, F8, WPT, CH, MODE>(a, src, a.rope + int64_t(pos0) * a.rope_dim, ps, count, live, head, page, scale,
-                                          codes, wi, s_max);
+        append_rows<T, F8, WPT, CH, MODE>(a, src, a.rope + int64_t(pos0) * a.rope_dim, ps, count, live, scale, codes, wi, s_max);
     else
-        append_rows<T, F8, WPT, CH, kNone>(a, src, nullptr, ps, count, live, head, page, scale, codes, wi, s_max);
+        append_rows<T, F8, WPT, CH, kNone>(a, src, nullptr, ps, count, live, scale, codes, wi, s_max);
+}
+
+// WPT > 1: a (sequence, page) item.  WPT 1 (few tokens a sequence): all pages of sequence `item`.
+template <typename T, bool F8, int WPT, int CH, Mode MODE>
+__device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, int part)
+{
+    __shared__ float s_max[kWarps];
+    if constexpr (WPT == 1) {
+        const int b = int(item), len = __ldg(a.seq_len + b);
+        const KvSpan span = kv_span(__ldg(a.cu_q + b), __ldg(a.cu_q + b + 1), len, a.M, a.capacity);
+#pragma unroll 1
+        for (int k = 0;; ++k) {
+            const KvPageSpan ps = kv_page_span(span, k, a.page_shift);
+            if (ps.count == 0) break;
+            append_page<T, F8, WPT, CH, MODE>(a, b, len, ps, part, s_max);
+        }
+    } else {
+        __shared__ int s_seq[4];
+        const int tid = threadIdx.x;
+        if (tid == 0) s_seq[0] = -1;
+        __syncthreads();
+        for (int b = tid; b < a.n_seqs; b += kThreads) {
+            const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
+            const int q0 = kv_clamp(lo, 0, a.M), q1 = kv_clamp(hi, q0, a.M);
+            if (kv_item_start(q0, b, a.page_shift) <= item && item < kv_item_start(q1, b + 1, a.page_shift)) {
+                s_seq[0] = b;
+                s_seq[1] = lo;
+                s_seq[2] = hi;
+                s_seq[3] = len;
+            }
+        }
+        __syncthreads();
+        const int b = s_seq[0];
+        if (b < 0) return;
+        const KvSpan span = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
+        const KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift), a.page_shift);
+        if (ps.count) append_page<T, F8, WPT, CH, MODE>(a, b, s_seq[3], ps, part, s_max);
+    }
 }
 
 // The queries of q_tokens tokens: kWarps / q_tokens warps take a token's heads in turn.
@@ -414,6 +454,7 @@ const void *append_kernel(Mode mode, bool many, bool wide)
     case kNone: return append_kernel<T, F8, kNone>(many, wide);
     case kPairs: return append_kernel<T, F8, kPairs>(many, wide);
     case kHalf: return append_kernel<T, F8, kHalf>(many, wide);
+    case kHalf2: return append_kernel<T, F8, kHalf2>(many, wide);
     default: return append_kernel<T, F8, kAny>(many, wide);
     }
 }
@@ -491,12 +532,13 @@ extern "C" wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t 
     // kHalf: partners and cos / sin at rope_dim / 2, a table row rope_dim values long; see Mode
     const Mode mode = !rope_dim                           ? kNone
                       : a.pairs                           ? (rope_dim % 4 == 0 ? kPairs : kAny)
-                      : rope_dim % 8 == 0 ? kHalf : kAny;
-    a.kv_items = (M >> a.page_shift) + 2 * batch->n_seqs;
+                      : rope_dim % 8 == 0 ? kHalf
+                      : rope_dim % 4 == 0 ? kHalf2 : kAny;
     // A page's rows go over all warps of a block where sequences bring many tokens, else one warp
     // takes each (head, keys or values).
     const bool many = M >= 4 * batch->n_seqs;
     a.parts = many ? 2 * cache->kv_heads : (2 * cache->kv_heads + kWarps - 1) / kWarps;
+    a.kv_items = many ? (M >> a.page_shift) + 2 * batch->n_seqs : batch->n_seqs;
     a.q_tokens = M <= 1024 ? 1 : kWarps;
     const int64_t blocks = a.kv_items * a.parts + (M + a.q_tokens - 1) / a.q_tokens;
     if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");

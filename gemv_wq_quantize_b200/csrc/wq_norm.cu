@@ -223,9 +223,13 @@ wq_status rmsnorm_quant(bool f8, const void *X, const void *residual, const void
     if (reinterpret_cast<uintptr_t>(a_scale) & 3) return fail(WQ_ERR_ALIGNMENT, "a_scale must be 4-byte aligned");
 
     NormArgs a{X, residual, gamma, h, Aq, a_scale, K / 8, eps};
+    // Few tokens: a vector a thread, for latency.  Many: four vectors a thread, so that more rows are
+    // in flight on an SM and a reduction joins fewer warps (8192 tokens of 4096: 55.8 -> 46.6 us;
+    // 128 tokens of 3200 would go from 3.2 to 3.6).
+    const int most = M > 2 * int64_t(device_info().sm_count) ? 128 : kNormThreads;
     int v = 0, threads = kNormThreads;
     for (int t : {1, 2, 4})
-        if (!v && a.K8 <= int64_t(t) * kNormThreads) {
+        if (!v && a.K8 <= int64_t(t) * (t < 4 ? most : kNormThreads)) {
             v = t;
             threads = int(((a.K8 + t - 1) / t + 31) / 32 * 32);
         }
