@@ -52,6 +52,7 @@ struct KvPageSpan {
 WQ_HD KvPageSpan kv_page_span(const KvSpan &s, int64_t k, int page_shift)
 {
     KvPageSpan r{0, 0, 0, 0};
+    if (k < 0) return r;                           // (sequences that overlap: no item's owner is certain)
     const int i0 = s.n > s.len ? s.n - s.len : 0;  // tokens without a place
     if (i0 >= s.n) return r;
     const int p0 = s.len - s.n + i0;               // first position written, >= 0
@@ -80,18 +81,22 @@ WQ_HD int64_t kv_scale_index(int64_t page, int head, int heads) { return page * 
 
 // ---- attention: row tiles and units -------------------------------------------------
 // The rows of (sequence, key head) are r = i * group + h (token i, query head h of the
-// group), in tiles of `rows`; a tile's keys are walked in units of `unit` tokens.  Every tile
+// group), in tiles of `rows`; a tile's keys are walked in units of 2^shift tokens.  Every tile
 // of a sequence counts the units of the sequence's whole length (at least one, so that tiles
 // without keys are written too).
 WQ_HD int64_t kv_tiles(int n, int group, int rows) { return (int64_t(n) * group + rows - 1) / rows; }
-WQ_HD int64_t kv_units(int len, int unit) { return len > 0 ? (int64_t(len) + unit - 1) / unit : 1; }
+WQ_HD int kv_units(int len, int shift) { return len > 0 ? int((int64_t(len) + (int64_t(1) << shift) - 1) >> shift) : 1; }
 
 // Blocks of `rows` rows for the sequences of a call without a sum over them: sequence b owns
 // the items from kv_row_item(q0_b, b) to kv_row_item(q0_{b+1}, b + 1), at least
 // floor(n * group / rows) + 1 >= kv_tiles(n, group, rows) of them.
 WQ_HD int64_t kv_row_item(int q0, int b, int group, int rows) { return int64_t(q0) * group / rows + b; }
 
-// Units [lo, hi) of the `total` that block `c` of `grid` takes.
-WQ_HD int64_t kv_share(int64_t total, int c, int grid) { return total / grid * c + total % grid * c / grid; }
+// Block c of `grid` takes the units kv_share(c) .. kv_share(c + 1) - 1 of `total` (grid below 2^16).
+WQ_HD int kv_share(int total, int c, int grid)
+{
+    const unsigned q = unsigned(total) / unsigned(grid), r = unsigned(total) % unsigned(grid);
+    return int(q * unsigned(c) + r * unsigned(c) / unsigned(grid));
+}
 
 }  // namespace wq

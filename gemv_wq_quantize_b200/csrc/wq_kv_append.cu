@@ -55,7 +55,7 @@ struct AppendArgs {
     wq_kv_cache c;
     const int32_t *cu_q, *seq_len, *block_table;
     int n_seqs, max_pages, M, q_heads;
-    int rope_len, rope_dim;
+    int rope_dim;
     int page_shift, pitch;
     int capacity;       // tokens that the block table's row holds
     int limit;          // positions below it have a place: min(capacity, rope_len)

@@ -62,7 +62,7 @@ constexpr int kParts = 4;                // 8-bit parts of a query value or weig
 constexpr int kUnitShift = 7;            // a unit: 128 keys, the granule of the split
 constexpr int kTileUnits = 4;            // what the start and end of a tile cost a block, in units
 constexpr int kLeastUnits = 1;           // of a share: less only adds partials
-constexpr int kMostUnits = 1 << 30;
+constexpr int kMostUnits = 0x7fffff00;   // of a call
 
 __device__ __forceinline__ uint64_t globaltimer()
 {
@@ -235,8 +235,8 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs &a, const int *before, 
     t.s = kv_span(__ldg(a.cu_q + lo), __ldg(a.cu_q + lo + 1), __ldg(a.seq_len + lo), a.M, a.capacity);
     const bool split = a.partials != nullptr;
     const int head_units = split ? kTileUnits : 0;
-    const int units = split ? head_units + max(1, int((int64_t(t.s.len) + (1 << shift) - 1) >> shift)) : 1;  // kv_units
-    const int tiles = (t.s.n * a.group + ROWS - 1) / ROWS;
+    const int units = split ? head_units + kv_units(t.s.len, shift) : 1;
+    const int tiles = int(kv_tiles(t.s.n, a.group, ROWS));
     const int item = (u - before[lo]) / units;  // (key head, tile) of the sequence
     const int begin = before[lo] + item * units, end = begin + units;
     next = min(end, u_end);
@@ -718,13 +718,6 @@ __device__ __forceinline__ void join_parts(const KvAttnArgs &a, Smem<NB, NR> &sm
 
 __device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
-// kv_share in 32 bits (total and grid * grid fit).
-__device__ __forceinline__ int share_of(int total, int c, int grid)
-{
-    const unsigned q = unsigned(total) / unsigned(grid), r = unsigned(total) % unsigned(grid);
-    return int(q * unsigned(c) + r * unsigned(c) / unsigned(grid));
-}
-
 template <bool F8, bool BF16, int NB, int NR>
 __device__ __forceinline__ void soft_role(const KvAttnArgs &a, Smem<NB, NR> &sm, Share<NR> share, uint32_t tbase, int total,
                                           int grid)
@@ -770,8 +763,8 @@ __device__ __forceinline__ void soft_role(const KvAttnArgs &a, Smem<NB, NR> &sm,
     if (tid == 0) {
         auto owner = [&](int x) {
             int c = min(grid - 1, int(float(x) * (float(grid) / float(total))));  // near the block that holds unit x
-            while (c > 0 && share_of(total, c, grid) > x) --c;
-            while (share_of(total, c + 1, grid) <= x) ++c;
+            while (c > 0 && kv_share(total, c, grid) > x) --c;
+            while (kv_share(total, c + 1, grid) <= x) ++c;
             return c;
         };
         int c0[2], parts[2];
@@ -844,8 +837,7 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
         const KvSpan s = kv_span(a.cu_q[b], a.cu_q[b + 1], len, a.M, a.capacity);
         if (len > a.capacity) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
         if (int64_t(s.n) * a.group > a.few_rows) return int64_t(0);
-        const int64_t units = max(int64_t(1), (int64_t(s.len) + (1 << shift) - 1) >> shift);  // kv_units
-        return kv_tiles(s.n, a.group, NR) * a.kv_heads * (split ? kTileUnits + units : 1);
+        return kv_tiles(s.n, a.group, NR) * a.kv_heads * (split ? kTileUnits + kv_units(s.len, shift) : 1);
     };
     int64_t mine, sum, all;
     for (;; ++shift) {  // (larger units where their count would not fit: more than 2^36 keys)
@@ -870,7 +862,9 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
         if (all <= kMostUnits || shift == 30) break;
         __syncthreads();
     }
-    const int total = int(min(all, int64_t(0x7fffffff)));
+    // (still more: sequences that overlap, so that there are more rows than the call has; none is done)
+    const int total = all <= kMostUnits ? int(all) : 0;
+    if (tid == 0 && all > kMostUnits) atomicCAS(&g_kv_attn_error, kErrNone, kErrRange);
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b < a.n_seqs) {
@@ -881,7 +875,7 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
     if (tid == 0) before[a.n_seqs] = total;
     // no more shares than units, so that no block between a tile's first and last is without one
     const int least = split ? kTileUnits + kLeastUnits : 1;
-    const int grid = min(int(gridDim.x), (total + least - 1) / least), cta = blockIdx.x;
+    const int grid = min(int(gridDim.x), total / least + (total % least != 0)), cta = blockIdx.x;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -891,7 +885,7 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
         if (warp == kMmaWarp) tc::tmem_dealloc(tbase, S::kTmem);
         return;
     }
-    const Share<NR> share{a, before, shift, share_of(total, cta, grid), share_of(total, cta + 1, grid)};
+    const Share<NR> share{a, before, shift, kv_share(total, cta, grid), kv_share(total, cta + 1, grid)};
     if (warp < kSoft / 32) {
         soft_role<F8, BF16, NB, NR>(a, sm, share, tbase, total, grid);
     } else if (warp == kCopyWarp) {
@@ -950,13 +944,13 @@ size_t kv_attn_rows_workspace()
 
 // Keys and values as (page and head, slot, byte): bytes behind the head are not read, the copy
 // fills zeros beyond the first dimension.
-wq_status encode_cache(CUtensorMap *km, CUtensorMap *vm, const KvAttnArgs &a, int row_bytes, int rows)
+wq_status encode_cache(CUtensorMap *km, CUtensorMap *vm, const KvAttnArgs &a, int rows)
 {
     const uint64_t dims[3] = {uint64_t(a.head_dim), uint64_t(1) << a.page_shift, uint64_t(a.num_pages) * a.kv_heads};
     const uint64_t strides[2] = {uint64_t(a.pitch), uint64_t(a.pitch) << a.page_shift};
-    const uint32_t box[3] = {uint32_t(row_bytes), uint32_t(rows), 1};
-    wq_status rc = encode_tmap(km, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.k, dims, strides, box, row_bytes);
-    return rc != WQ_OK ? rc : encode_tmap(vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.v, dims, strides, box, row_bytes);
+    const uint32_t box[3] = {128, uint32_t(rows), 1};
+    wq_status rc = encode_tmap(km, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.k, dims, strides, box, 128);
+    return rc != WQ_OK ? rc : encode_tmap(vm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.v, dims, strides, box, 128);
 }
 
 void set_attn_launch(PreparedLaunch &L, const void *fn, unsigned blocks, int threads, size_t smem, const CUtensorMap &km,
@@ -984,7 +978,7 @@ wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
     if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem + (kKvMaxSeqs + 1) * sizeof(int))) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_rows_kernel)");
     CUtensorMap km, vm;
-    wq_status rc = encode_cache(&km, &vm, a, 128, std::min(1 << a.page_shift, kKeys));
+    wq_status rc = encode_cache(&km, &vm, a, std::min(1 << a.page_shift, kKeys));
     if (rc != WQ_OK) return rc;
     PreparedLaunch L;
     set_attn_launch(L, p.fn, unsigned(device_info().sm_count * p.per_sm), kThreads, smem, km, vm, a);

@@ -28,9 +28,9 @@ struct KvAttnArgs {
     unsigned *arrivals;
 };
 
-// The cache's codes as tensor maps of boxes of `rows` keys by row_bytes (64 or 128, swizzled as
-// wide), and a launch with (key map, value map, arguments).
-wq_status encode_cache(CUtensorMap *km, CUtensorMap *vm, const KvAttnArgs &a, int row_bytes, int rows);
+// The cache's codes as tensor maps of boxes of `rows` keys by 128 bytes, swizzled as wide, and a
+// launch with (key map, value map, arguments).
+wq_status encode_cache(CUtensorMap *km, CUtensorMap *vm, const KvAttnArgs &a, int rows);
 void set_attn_launch(PreparedLaunch &L, const void *fn, unsigned blocks, int threads, size_t smem, const CUtensorMap &km,
                      const CUtensorMap &vm, const KvAttnArgs &a);
 

@@ -642,7 +642,6 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     volatile int *abort = &abort_flag;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
-    grid_dep_launch();  // (not before: see KvAttnArgs::behind_tiles)
 
     const int64_t item = blockIdx.x / a.kv_heads;
     if (tid == 0) {
@@ -708,6 +707,9 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    // Not before the wait above (see KvAttnArgs::behind_tiles), and not before the Tensor Memory is
+    // taken: a later kernel that took all of it and waited for this one would never see it end.
+    grid_dep_launch();
     const uint32_t tbase = tmem_slot;
 
     if (warp < kSoftWarps) {
@@ -748,7 +750,7 @@ wq_status kv_attn_tiles(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st
     const int64_t blocks = kv_row_item(a.M, a.n_seqs, a.group, kRows) * a.kv_heads;
     if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
     CUtensorMap km, vm;
-    wq_status rc = encode_cache(&km, &vm, a, 128, std::min(1 << a.page_shift, kKeys));
+    wq_status rc = encode_cache(&km, &vm, a, std::min(1 << a.page_shift, kKeys));
     if (rc != WQ_OK) return rc;
     PreparedLaunch L;
     set_attn_launch(L, fn, unsigned(blocks), kThreads, size_t(smem), km, vm, a);

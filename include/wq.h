@@ -242,8 +242,7 @@ wq_status w8a8_fp8_gemm_fused(const void *A, wq_dtype a_dt, const uint8_t *Wq, c
 /* ---- The steps of a decoder layer between its matmuls: the norm in front of a projection, the
  * append of keys and values behind the QKV projection, and attention over the cached keys and
  * values.  They read and write what the matmuls above write and read: 16-bit rows, per-token
- * 8-bit activations, and a key / value cache in the activations' two 8-bit formats.  (The
- * survey pages name these steps as part of the serving stack around the matmul.) */
+ * 8-bit activations, and a key / value cache in the activations' two 8-bit formats. */
 
 /* RMS norm with the residual's addition, and its output quantized per token: the input that
  * act_quant_int8 / act_quant_fp8 would otherwise read again.  For every token m:
@@ -291,11 +290,13 @@ typedef struct {
  * A row with a negative position (an idle slot of a fixed-size batch: seq_len 0) has no place:
  * kv_append stores nothing for it and kv_attention gives zeros.  Rows from cu_q[n_seqs] on are
  * left as they were.  Sequences may share pages that they only read; a page that a call writes
- * belongs to one sequence of the call.
+ * belongs to one sequence of the call, and to one place in its table.
  * What the host cannot check is checked on the device: a needed block-table entry outside
  * 0 .. num_pages - 1, or seq_len beyond max_pages * page_size or beyond the rope table, sets the
  * device error word to 3 (wq_device_error); the tokens concerned are left out, nothing is
- * accessed out of range, and results of those sequences are not valid.  cu_q is cut to 0..M. */
+ * accessed out of range, and results of those sequences are not valid.  cu_q does not decrease and
+ * is cut to 0..M; sequences that overlap are not accessed out of range either, but their results
+ * are not valid. */
 typedef struct {
     const int32_t *cu_q;
     const int32_t *seq_len;

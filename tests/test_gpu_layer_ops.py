@@ -236,6 +236,11 @@ APPEND = [
     ([40, 40], [61, 40], 6, 3, 80, 32, 6, "half"),
     ([33, 1, 12], [64, 2, 12], 2, 2, 192, 64, 96, "pairs"),
     ([25], [77], 2, 2, 52, 16, 0, "half"),                              # no rotation
+    ([3, 1, 2, 0, 1], [33, 17, 3, 9, 1], 6, 3, 100, 16, 100, "half"),   # few tokens, over a page's end
+    ([0] * 20 + [40], [5] * 20 + [55], 4, 2, 128, 16, 36, "half"),      # few on average, many at once
+    ([0] * 30 + [100], [0] * 30 + [100], 2, 1, 256, 256, 256, "half"),
+    ([9], [60], 2, 1, 132, 64, 132, "half"),
+    ([2, 1], [40, 16], 3, 1, 36, 32, 18, "half"),
 ]
 
 
@@ -563,6 +568,51 @@ def test_bad_pages_and_lengths_are_reported():
     _append(s, qkv, np.ones((20, 64), np.float32), "half", cache, batch)
     torch.cuda.synchronize()
     assert wq.device_error() == 3 and torch.equal(cache.k, k0)
+
+
+def test_overlapping_sequences_stay_inside_the_call():
+    """cu_q that decreases: not valid, but nothing outside the call is written; and where the rows
+    of all sequences together would be beyond counting, the call does nothing and says so."""
+    s = Setup([20, 3, 30], [40, 9, 64], 4, 2, 64, 16, "fp16", "int8", seed=5, tail=4).fill([40, 9, 64])
+    s.table[s.table == 1 << 30] = 0
+    for cu in ([0, 53, 2, 53], [30, 10, 0, 53], [-5, 60, -7, 1 << 30]):
+        cache, batch = s.device()
+        batch.cu_q.copy_(torch.tensor(cu, dtype=torch.int32))
+        _attend(s, s.q(), cache, batch)
+        _append(s, s.qkv(), s.rope(64), "half", cache, batch)
+    torch.cuda.synchronize()
+    wq.device_error()
+    n, M = 4096, 65536
+    cache = wq.make_kv_cache(2, 16, 64, 16, format=wq.FMT_INT)
+    cu = torch.tensor([0, M] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+    batch = wq.KVBatch(cu, torch.ones(n, dtype=torch.int32, device="cuda"), torch.zeros(n, 1, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(M, 64, 16, dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, MARK)
+    wq.kv_attention(q, cache, batch, out=out, workspace=wq.make_workspace(wq.kv_attention_workspace_size(M, 64, cache, batch)))
+    torch.cuda.synchronize()
+    assert wq.device_error() == 3 and (out == MARK).all()
+
+
+def test_attention_of_two_streams_at_once():
+    """Few and many rows, each with a workspace of its own, beside each other: the bits of one
+    after the other."""
+    few = Setup([1] * 6, [3000, 1, 700, 2500, 64, 900], 8, 2, 64, 32, "bf16", "fp8", seed=3).fill([3000, 1, 700, 2500, 64, 900])
+    many = Setup([300, 1, 90], [900, 2000, 90], 8, 1, 64, 64, "fp16", "int8", seed=4).fill([900, 2000, 90])
+    runs = []
+    for s in (few, many):
+        cache, batch = s.device()
+        runs.append((s, _dev(s.q(), s.dt), cache, batch,
+                     wq.make_workspace(wq.kv_attention_workspace_size(s.M, s.q_heads, cache, batch))))
+    alone = [wq.kv_attention(q, cache, batch, workspace=ws) for _, q, cache, batch, ws in runs]
+    outs = [[torch.empty_like(a) for _ in range(10)] for a in alone]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for i in range(10):
+        for (s, q, cache, batch, ws), st, o in zip(runs, streams, outs):
+            wq.kv_attention(q, cache, batch, out=o[i], workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert all(torch.equal(a, x) for x in o)
 
 
 # ---------------------------------------------------------------- together

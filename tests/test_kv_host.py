@@ -28,9 +28,9 @@ long long page_ok(int e, long long n) { return kv_page_ok(e, n); }
 long long code_offset(long long p, int h, int s, int H, int sh, int pitch) { return kv_code_offset(p, h, s, H, sh, pitch); }
 long long scale_index(long long p, int h, int H) { return kv_scale_index(p, h, H); }
 long long tiles(int n, int g, int r) { return kv_tiles(n, g, r); }
-long long units(int len, int u) { return kv_units(len, u); }
+long long units(int len, int shift) { return kv_units(len, shift); }
 long long row_item(int q0, int b, int g, int r) { return kv_row_item(q0, b, g, r); }
-long long share(long long t, int c, int g) { return kv_share(t, c, g); }
+long long share(int t, int c, int g) { return kv_share(t, c, g); }
 }
 """
 
@@ -45,7 +45,7 @@ def kv(tmp_path_factory):
     lib = ctypes.CDLL(str(so))
     for f in ("item_start", "page_ok", "code_offset", "scale_index", "tiles", "units", "share", "row_item"):
         getattr(lib, f).restype = ctypes.c_longlong
-    for f, t in (("page_ok", [ctypes.c_int, ctypes.c_longlong]), ("share", [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]),
+    for f, t in (("page_ok", [ctypes.c_int, ctypes.c_longlong]), ("share", [ctypes.c_int] * 3),
                  ("code_offset", [ctypes.c_longlong] + [ctypes.c_int] * 5), ("scale_index", [ctypes.c_longlong] + [ctypes.c_int] * 2),
                  ("page_span", [ctypes.c_int] * 3 + [ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p])):
         getattr(lib, f).argtypes = t
@@ -96,6 +96,10 @@ def test_items_cover_every_new_token_once(kv, shift):
                     assert got == want, (n, past, missing, q0)
 
 
+def test_an_item_before_the_sequence_is_idle(kv):
+    assert _page_span(kv, 0, 40, 40, -1, 4) == (0, 0, 0, 0)
+
+
 def test_item_starts_never_overlap(kv):
     r = np.random.default_rng(0)
     for shift in (4, 6, 8):
@@ -124,12 +128,13 @@ def test_pages_offsets_and_shares(kv):
     assert sorted(kv.scale_index(p, h, heads) for p in range(pages) for h in range(heads)) == list(range(6))
     # beyond 32 bits
     assert kv.code_offset(2 ** 31 - 1, 7, 15, 8, 8, 256) == (((2 ** 31 - 1) * 8 + 7) * 256 + 15) * 256
-    for total, grid in itertools.product((1, 2, 147, 148, 149, 1000, 2 ** 40 + 7), (1, 2, 147, 148, 444)):
+    for total, grid in itertools.product((0, 1, 2, 147, 148, 149, 1000, 2 ** 31 - 1), (1, 2, 147, 148, 296, 1001)):
         cuts = [kv.share(total, c, grid) for c in range(grid + 1)]
         assert cuts[0] == 0 and cuts[-1] == total and all(0 <= b - a <= total // grid + 1 for a, b in zip(cuts, cuts[1:]))
         if grid <= total:
             assert all(b > a for a, b in zip(cuts, cuts[1:]))  # no share is empty
-    assert kv.tiles(0, 4, 8) == 0 and kv.tiles(3, 5, 8) == 2 and kv.units(0, 64) == 1 and kv.units(65, 64) == 2
+    assert kv.tiles(0, 4, 8) == 0 and kv.tiles(3, 5, 8) == 2 and kv.units(0, 6) == 1 and kv.units(65, 6) == 2
+    assert kv.units(2 ** 31 - 1, 7) == 2 ** 24 and kv.units(2 ** 31 - 1, 30) == 2
 
 
 # ---------------------------------------------------------------- refusals of the C entry points
