@@ -30,6 +30,7 @@
 // partial sums in the workspace; the last block to arrive adds them in the order of their keys,
 // so the result does not depend on which block that is.
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -102,7 +103,7 @@ struct Smem {
     int first[2], parts[2];      // the tiles that this block left partials of
     int abort;
     uint32_t tmem;
-    // then the unit counts of all sequences up to each (n_seqs + 1)
+    int before[1];               // the units of all sequences before each: n_seqs + 1
 };
 
 // A bounded wait: about 2 s, or `after` (nanoseconds) once another role gave up.  wait_warp: one
@@ -801,7 +802,7 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t fin;
     Smem<NB, NR> &sm = *reinterpret_cast<Smem<NB, NR> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int *before = reinterpret_cast<int *>(&sm + 1);  // units of sequences < b
+    int *before = sm.before;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -912,13 +913,16 @@ kv_attn_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constan
 struct RowsPlan {
     const void *fn;
     int per_sm;
-    size_t smem;  // without the unit counts
+    size_t smem;  // without the counts of `before`
 };
 
 template <bool F8, bool BF16, int NB, int NR>
 RowsPlan rows_plan()
 {
-    return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, NB, NR>), Shape<NB, NR>::kPerSm, sizeof(Smem<NB, NR>) + 1024};
+    using M = Smem<NB, NR>;
+    constexpr size_t smem = offsetof(M, before) + 1024;
+    static_assert(smem + (kKvMaxSeqs + 1) * sizeof(int) + sizeof(uint64_t) <= 232448, "a block's shared memory (and `fin`)");
+    return {reinterpret_cast<const void *>(kv_attn_rows_kernel<F8, BF16, NB, NR>), Shape<NB, NR>::kPerSm, smem};
 }
 
 template <bool F8, bool BF16>
@@ -1033,10 +1037,15 @@ extern "C" wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t
         a.arrivals = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) + ws_scratch_bytes());
     }
     // Sequences with up to kFewRows rows per key head are bound by reading their keys once and go
-    // to the key-split kernel, the others to the tile kernel (heads up to 128).  One launch
-    // where sequences bring that few rows on average, right for any distribution.
+    // to the key-split kernel, the others to the tile kernel.  One launch where sequences bring that
+    // few rows on average, right for any distribution; and where the call's rows are so few that
+    // tiles would leave most SMs idle, even if each key is read for several tiles of 16 rows.
+    // Tiles against split, us: heads of 128, 3000 keys, 1280 rows in all 80 / 44, 3200 rows 83 / 81,
+    // 6400 rows 80 / 134; 64 rows and 20000 keys 382 / 36; heads of 256, 1280 rows 88 / 67, 3200
+    // rows 89 / 128.
     const bool bf16 = dt == WQ_BF16, f8 = cache->format == WQ_FMT_E4M3;
-    const bool tiles = a.head_dim <= 128 && M * a.group > kFewRows * batch->n_seqs;
+    const int64_t idle = int64_t(a.head_dim <= 128 ? 24 : 16) * device_info().sm_count;
+    const bool tiles = M * a.group > kFewRows * batch->n_seqs && M * q_heads > idle;
     a.few_rows = tiles ? kFewRows : 0x7fffffff;
     if (tiles) {
         rc = kv_attn_tiles(a, bf16, f8, stream);

@@ -43,12 +43,8 @@ int kv_tiles_read_error()
 namespace {
 
 constexpr int kTile = 128;           // rows of a tile: MMA M
-constexpr int kRows = 2 * kTile;     // rows of a block
-constexpr int kKeys = 128;           // keys of a step
-constexpr int kGroups = kKeys / 16;  // a group of 16 keys lies in one page
-constexpr int kSoftWarps = 8, kConvWarps = 4;  // (14 warps leave 128 registers a thread)
-constexpr int kConvThreads = 32 * kConvWarps;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kMaxGroups = 8;        // groups of 16 keys of a step (a group lies in one page)
+constexpr int kMmaWarp = 12, kCopyWarp = 13;  // (14 warps leave 128 registers a thread)
 constexpr int kThreads = 32 * (kCopyWarp + 1);
 __device__ __forceinline__ float log2_approx(float x)
 {
@@ -89,21 +85,37 @@ struct Bars {
     uint64_t raw_k_full, raw_k_free, raw_v_full, raw_v_free, fin;
 };
 struct Scales {
-    float k[kRing][kGroups];       // key scale * |sm_scale| * log2 e
-    float v[kRing][kGroups];       // value scale, its logarithm and inverse
-    float log_v[kRing][kGroups], inv_v[kRing][kGroups];
+    float k[kRing][kMaxGroups];    // key scale * |sm_scale| * log2 e
+    float v[kRing][kMaxGroups];    // value scale, its logarithm and inverse
+    float log_v[kRing][kMaxGroups], inv_v[kRing][kMaxGroups];
     float v_max[kRing];
     uint32_t dead[kRing];          // groups whose block-table entry is no page
     int plain[kRing];              // no dead groups, all value scales positive normal numbers
 };
 
+// DT: the head's size rounded up to 64, 128 or 256.  Up to 128: two tiles of 128 rows, steps of 128
+// keys.  256: the sums of one tile take half of the Tensor Memory and two steps of 128 keys do not fit
+// shared memory, so one tile in steps of 64 keys, with scores of two steps in Tensor Memory so that
+// products and softmax still overlap; the second tile's warps widen codes instead.
 template <int DT>
 struct Layout {
-    static constexpr int kAtom = 128 * 128;            // 128 rows of 64 binary16
-    static constexpr int kQ = DT / 64 * kAtom;         // a query tile, a key step
-    static constexpr int kV = 2 * DT * 128;            // DT rows of 128 keys
-    static constexpr int kRaw = kKeys * 128;           // codes of a key step, 128 bytes a key
-    static constexpr int kBytes = 2 * kQ + 2 * kQ + 2 * kV + 2 * kRaw;
+    static constexpr bool kTwo = DT <= 128;
+    static constexpr int kRows = kTwo ? 2 * kTile : kTile;  // of a block
+    static constexpr int kKeys = kTwo ? 128 : 64;           // of a step
+    static constexpr int kGroups = kKeys / 16;
+    static constexpr int kSoftWarps = kTwo ? 8 : 4, kConvWarps = kMmaWarp - kSoftWarps;
+    static constexpr int kBoxes = DT <= 128 ? 1 : 2;        // boxes of 128 bytes of a key
+    static constexpr int kAtom = kTile * 128;               // 128 query rows of 64 binary16
+    static constexpr int kQ = DT / 64 * kAtom;              // a query tile
+    static constexpr int kKAtom = kKeys * 128;              // the same of a step's keys
+    static constexpr int kK = DT / 64 * kKAtom;
+    static constexpr int kV = 2 * DT * kKeys;               // DT rows of keys
+    static constexpr int kRaw = kKeys * 128 * kBoxes;       // codes of a step
+    static constexpr int kBytes = kRows / kTile * kQ + 2 * kK + 2 * kV + 2 * kRaw;
+    // the scores of (tile, step): their columns, and the parity of their barriers
+    static constexpr uint32_t kSCols = kTwo ? 128 : 64;
+    __device__ static __forceinline__ int slot(int tile, int j) { return kTwo ? tile : j & 1; }
+    __device__ static __forceinline__ uint32_t parity(int j) { return (kTwo ? j : j >> 1) & 1; }
 };
 
 __device__ __forceinline__ uint64_t globaltimer()
@@ -145,15 +157,17 @@ struct Item {
 };
 
 // ------------------------------------------------------------------ codes to shared memory
-// A step's codes arrive as one box per page part, 128 bytes a key (zeros behind the head), in the
-// 128-byte swizzle; lanes look up a page each.  Lanes 0 .. 7 also bring a group's scales.
+// A step's codes arrive as boxes per page part of 128 bytes a key (zeros behind the head), in the
+// 128-byte swizzle; lanes look up a page each, of a box or of a group and its scales.
+template <int DT>
 __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, const CUtensorMap *km, const CUtensorMap *vm,
                                           uint8_t *kraw, uint8_t *vraw, Scales &sc, Bars &bar, volatile int *abort)
 {
+    constexpr int kKeys = Layout<DT>::kKeys, kGroups = Layout<DT>::kGroups, kBoxes = Layout<DT>::kBoxes;
     const int lane = threadIdx.x % 32;
     const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
     const int box_rows = min(1 << a.page_shift, kKeys), boxes = kKeys / box_rows;
-    // lane l: the page of box l, lane 8 + l: that of group l
+    // lane l: the page of box l, lane kGroups + l: that of group l
     const int my_key = lane < kGroups ? lane * box_rows : (lane - kGroups) * 16;
     const bool boxed = lane < boxes, grouped = lane >= kGroups && lane < 2 * kGroups;
     auto entry_of = [&](int step) {
@@ -172,17 +186,23 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, co
             vs = __ldg(a.v_scale + z);
         }
         if (j + 1 < t.steps) entry = entry_of(j + 1);
-        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, boxed && z >= 0))) * uint32_t(box_rows) * 128u;
+        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, boxed && z >= 0))) * uint32_t(box_rows * 128 * kBoxes);
         const int y = key & ((1 << a.page_shift) - 1);
         if (j && !wait_warp(&bar.raw_k_free, (j - 1) & 1, abort)) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar.raw_k_full, bytes);
         __syncwarp();
-        if (boxed && z >= 0) tma_load_3d(kraw + lane * box_rows * 128, km, 0, y, z, &bar.raw_k_full);
+        if (boxed && z >= 0)
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c)
+                tma_load_3d(kraw + c * kKeys * 128 + lane * box_rows * 128, km, 128 * c, y, z, &bar.raw_k_full);
         sent_k = j + 1;
         if (j && !wait_warp(&bar.raw_v_free, (j - 1) & 1, abort)) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar.raw_v_full, bytes);
         __syncwarp();
-        if (boxed && z >= 0) tma_load_3d(vraw + lane * box_rows * 128, vm, 0, y, z, &bar.raw_v_full);
+        if (boxed && z >= 0)
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c)
+                tma_load_3d(vraw + c * kKeys * 128 + lane * box_rows * 128, vm, 128 * c, y, z, &bar.raw_v_full);
         sent_v = j + 1;
         // ---- scales
         const int set = j % kRing, g = lane - kGroups;
@@ -217,37 +237,40 @@ template <bool F8, int DT>
 __device__ __noinline__ void convert_role(const KvAttnArgs &a, const Item &t, const uint8_t *kraw, const uint8_t *vraw, uint8_t *ksm,
                              uint8_t *vsm, const Scales &sc, Bars &bar, volatile int *abort)
 {
-    constexpr int kPerRow = DT / 16;                  // 16-byte chunks of a key
-    constexpr int kPass = kConvThreads / kPerRow;     // keys of a pass
-    constexpr int kKp = kKeys / kPass;                // passes: 8 (DT 128) or 4
-    constexpr int kVt = DT / 8 / kConvWarps;          // value tasks (8 keys x 4 dimensions) of a thread
-    const int ct = threadIdx.x - 32 * kSoftWarps, cw = ct / 32, lane = ct % 32;
+    using L = Layout<DT>;
+    constexpr int kKeys = L::kKeys;
+    constexpr int kPerRow = DT / 16;                        // 16-byte chunks of a key
+    constexpr int kPass = 32 * L::kConvWarps / kPerRow;     // keys of a pass
+    constexpr int kKp = kKeys / kPass;                      // passes: 8 (DT 128) or 4
+    constexpr int kKeyWarps = kKeys / 32, kDimWarps = L::kConvWarps / kKeyWarps;
+    constexpr int kVt = DT / 32 / kDimWarps;                // value tasks (8 keys x 4 dimensions) of a thread
+    const int ct = threadIdx.x - 32 * L::kSoftWarps, cw = ct / 32, lane = ct % 32;
     const int chunk = ct % kPerRow, krow = ct / kPerRow;
     // values: a warp takes 32 keys; its lanes 8 keys x 4 dimensions each, so that the transposed
     // 16-byte stores are free of conflicts
-    const int tg = lane % 8 / 2, dg = 2 * (lane / 8) + lane % 2, vkey = 32 * cw + 8 * tg;
+    const int tg = lane % 8 / 2, dg = 2 * (lane / 8) + lane % 2, vkey = 32 * (cw % kKeyWarps) + 8 * tg;
     for (int j = 0; j < t.steps; ++j) {
         const int buf = j & 1;
-        uint8_t *kb = ksm + buf * Layout<DT>::kQ, *vb = vsm + buf * Layout<DT>::kV;
+        uint8_t *kb = ksm + buf * Layout<DT>::kK, *vb = vsm + buf * Layout<DT>::kV;
         // ---- keys
         if (!wait_warp(&bar.raw_k_full, j & 1, abort)) return;
         if (j >= 2 && !wait_warp(&bar.k_free[buf], ((j >> 1) - 1) & 1, abort)) return;
 #pragma unroll 1
         for (int i = 0; i < kKp; ++i) {
             const int r = krow + kPass * i;
-            const uint4 raw = lds128(kraw + r * 128 + ((chunk ^ (r & 7)) << 4));
+            const uint4 raw = lds128(kraw + chunk / 8 * (kKeys * 128) + r * 128 + (((chunk % 8) ^ (r & 7)) << 4));
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             if constexpr (!F8) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) w[x] ^= 0x80808080u;
             }
-            uint8_t *row = kb + chunk / 4 * Layout<DT>::kAtom + r * 128;
+            uint8_t *row = kb + chunk / 4 * Layout<DT>::kKAtom + r * 128;
             const uint4 lo = make_uint4(widen<F8, 0>(w[0]), widen<F8, 1>(w[0]), widen<F8, 0>(w[1]), widen<F8, 1>(w[1]));
             const uint4 hi = make_uint4(widen<F8, 0>(w[2]), widen<F8, 1>(w[2]), widen<F8, 0>(w[3]), widen<F8, 1>(w[3]));
             const int c = 2 * (chunk % 4);
-            // the lanes of the upper 64 dimensions store their halves in the other order: the two
-            // atoms share banks
-            const bool swap = chunk >= 4;
+            // the lanes of every other 64 dimensions store their halves in the other order: the atoms
+            // share banks
+            const bool swap = chunk / 4 % 2;
             sts128(row + (((c + swap) ^ (r & 7)) << 4), swap ? hi : lo);
             sts128(row + (((c + !swap) ^ (r & 7)) << 4), swap ? lo : hi);
         }
@@ -265,11 +288,11 @@ __device__ __noinline__ void convert_role(const KvAttnArgs &a, const Item &t, co
         if (F8 && wait_warp(&bar.sc_full[j % kRing], (j / kRing) & 1, abort) && (sc.dead[j % kRing] >> (vkey / 16) & 1)) left = 0;
 #pragma unroll 1
         for (int i = 0; i < kVt; ++i) {
-            const int d = 32 * i + 4 * dg;
+            const int d = cw / kKeyWarps * (DT / kDimWarps) + 32 * i + 4 * dg;
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                w[e] = lds32(vraw + (vkey + e) * 128 + (((d >> 4) ^ e) << 4) + (d & 15));
+                w[e] = lds32(vraw + d / 128 * (kKeys * 128) + (vkey + e) * 128 + (((d % 128 / 16) ^ e) << 4) + (d & 15));
             if (F8 && left < 8) {
                 // slots behind the last key hold anything, e4m3 NaN codes among it
 #pragma unroll
@@ -310,27 +333,30 @@ template <int DT>
 __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uint32_t kaddr, uint32_t vaddr, Bars &bar,
                          uint32_t tbase, volatile int *abort)
 {
-    const uint32_t iqk = tc::idesc_f16(false, kTile, kKeys), ipv = tc::idesc_f16(false, kTile, DT);
+    using L = Layout<DT>;
+    const uint32_t iqk = tc::idesc_f16(false, kTile, L::kKeys), ipv = tc::idesc_f16(false, kTile, DT);
     // descriptors differ in their address field only: the offsets below are constants added to the
     // low word
     const uint64_t dq = tc::sdesc_sw128(qaddr), dk = tc::sdesc_sw128(kaddr), dv = tc::sdesc_sw128(vaddr);
     const uint32_t high = uint32_t(dq >> 32), q_lo = uint32_t(dq), k_lo = uint32_t(dk), v_lo = uint32_t(dv);
     auto desc = [&](uint32_t lo) { return uint64_t(high) << 32 | lo; };
-    auto qk = [&](int tile, int buf) {
-        const uint32_t q = q_lo + uint32_t(tile * Layout<DT>::kQ >> 4), k = k_lo + uint32_t(buf * Layout<DT>::kQ >> 4);
+    auto qk = [&](int tile, int j) {
+        const uint32_t q = q_lo + uint32_t(tile * L::kQ >> 4), k = k_lo + uint32_t((j & 1) * L::kK >> 4);
 #pragma unroll
         for (int i = 0; i < DT / 16; ++i) {
-            const uint32_t off = uint32_t(((i >> 2) * Layout<DT>::kAtom + (i & 3) * 32) >> 4);
-            tc::mma_f16_ss(tbase + kScol + 128 * tile, desc(q + off), desc(k + off), iqk, i > 0);
+            const uint32_t at = uint32_t(i & 3) * 32;
+            tc::mma_f16_ss(tbase + kScol + L::kSCols * L::slot(tile, j), desc(q + (((i >> 2) * L::kAtom + at) >> 4)),
+                           desc(k + (((i >> 2) * L::kKAtom + at) >> 4)), iqk, i > 0);
         }
-        tc::commit(&bar.s_full[tile]);
+        tc::commit(&bar.s_full[L::slot(tile, j)]);
     };
-    auto pv = [&](int tile, int buf, bool first) {
-        const uint32_t v = v_lo + uint32_t(buf * Layout<DT>::kV >> 4);
+    auto pv = [&](int tile, int j) {
+        const uint32_t v = v_lo + uint32_t((j & 1) * L::kV >> 4);
 #pragma unroll
-        for (int i = 0; i < kKeys / 16; ++i) {
+        for (int i = 0; i < L::kGroups; ++i) {
             const uint32_t off = uint32_t(((i >> 2) * (DT * 128) + (i & 3) * 32) >> 4);
-            tc::mma_f16_ts(tbase + kOcol + 128 * tile, tbase + kScol + 128 * tile + 8 * i, desc(v + off), ipv, !first || i > 0);
+            tc::mma_f16_ts(tbase + kOcol + 128 * tile, tbase + kScol + L::kSCols * L::slot(tile, j) + 8 * i, desc(v + off), ipv,
+                           j > 0 || i > 0);
         }
         tc::commit(&bar.o_done[tile]);
     };
@@ -340,6 +366,22 @@ __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uin
         if (t.steps_of[tile]) qk(tile, 0);
     tc::commit(&bar.k_free[0]);
     bool ok = true;
+    if constexpr (!L::kTwo) {
+        // the next step's scores go over the weights of the step before, whose product is in the pipe
+        for (int j = 0; j < t.steps; ++j) {
+            if (j + 1 < t.steps) {
+                if (!wait(&bar.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort)) break;
+                tc::fence_after_sync();
+                qk(0, j + 1);
+                tc::commit(&bar.k_free[(j + 1) & 1]);
+            }
+            if (!wait(&bar.p_full[j & 1], L::parity(j), abort) || !wait(&bar.v_full[j & 1], (j >> 1) & 1, abort)) break;
+            tc::fence_after_sync();
+            pv(0, j);
+            tc::commit(&bar.v_free[j & 1]);
+        }
+        ok = false;
+    }
     for (int j = 0; j < t.steps && ok; ++j) {
         const int buf = j & 1, nbuf = buf ^ 1;
         bool have_v = false, have_k = false;
@@ -349,7 +391,7 @@ __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uin
             if (!ok) break;
             have_v = true;
             tc::fence_after_sync();
-            pv(tile, buf, j == 0);
+            pv(tile, j);
             if (j + 1 < t.steps_of[tile]) {
                 if (!have_k) {
                     ok = wait(&bar.k_full[nbuf], ((j + 1) >> 1) & 1, abort);
@@ -357,7 +399,7 @@ __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uin
                     have_k = true;
                     tc::fence_after_sync();
                 }
-                qk(tile, nbuf);  // behind the tile's second product in the pipe: it may overwrite the weights
+                qk(tile, j + 1);  // behind the tile's second product in the pipe: it may overwrite the weights
             }
         }
         if (!ok) break;
@@ -372,17 +414,17 @@ __device__ void mma_role(const KvAttnArgs &a, const Item &t, uint32_t qaddr, uin
 // The weights of a step in one pass over its scores (see softmax_role), stored over them if all of
 // the warp fit binary16 (true; any: whatever they are), else nothing is.  MASKED: some row sees fewer
 // than all keys.
-template <bool MASKED>
+template <bool MASKED, int GROUPS>
 __device__ __forceinline__ bool weights_once(uint32_t scol, const float *ks, const float *log_v, const float *inv_v,
                                              float unscale, float shift, int left, float &lsum, bool any)
 {
-    uint32_t p[4][16], s[2][16];
+    uint32_t p[GROUPS / 2][16], s[2][16];
     float most = 0.f;
     tc::ld_32x32b_x16(scol, s[0]);
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < GROUPS; ++g) {
         tc::wait_ld();
-        if (g + 1 < kGroups) tc::ld_32x32b_x16(scol + 16 * (g + 1), s[(g + 1) & 1]);
+        if (g + 1 < GROUPS) tc::ld_32x32b_x16(scol + 16 * (g + 1), s[(g + 1) & 1]);
         if (MASKED)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -404,7 +446,7 @@ __device__ __forceinline__ bool weights_once(uint32_t scol, const float *ks, con
     }
     if (!__all_sync(0xffffffffu, most == 0.f || any)) return false;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tc::st_32x32b_x16(scol + 16 * c, p[c]);
+    for (int c = 0; c < GROUPS / 2; ++c) tc::st_32x32b_x16(scol + 16 * c, p[c]);
     tc::wait_st();
     return true;
 }
@@ -420,7 +462,7 @@ __device__ __forceinline__ bool new_references(uint32_t scol, uint32_t ocol, con
 {
     float mx = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < Layout<DT>::kGroups / 2; ++c) {
         uint32_t s[32];
         tc::ld_32x32b_x32(scol + 32 * c, s);
         tc::wait_ld();
@@ -467,12 +509,13 @@ __device__ __forceinline__ bool new_references(uint32_t scol, uint32_t ocol, con
 }
 
 // The weights of a step with groups that are no pages or value scales that have no logarithm.
+template <int GROUPS>
 __device__ __forceinline__ void weights_any(uint32_t scol, const Scales &sc, int set, float unscale, int left, uint32_t dead,
                                             float m, float vref, float &l)
 {
     const float base = m == -INFINITY ? 0.f : m - kRaise, inv = vref > 0.f ? 1.f / vref : 0.f;
 #pragma unroll 1
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < GROUPS; ++g) {
         uint32_t s[16], p[8];
         tc::ld_32x32b_x16(scol + 16 * g, s);
         tc::wait_ld();
@@ -499,6 +542,8 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
                              uint32_t tbase, volatile int *abort)
 {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    using L = Layout<DT>;
+    constexpr int kKeys = L::kKeys, kGroups = L::kGroups, kBoxes = L::kBoxes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, tile = warp / 4;
     if (tile >= t.tiles) return;
     const int r = 32 * (warp % 4) + lane, row = tile * kTile + r;
@@ -507,43 +552,60 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
     const int64_t at = (int64_t(t.s.q0 + i) * a.q_heads + t.head * a.group + h) * a.head_dim;
     const int seen = live ? t.s.len - t.s.n + i + 1 : 0;
     const uint32_t tlane = tbase + (uint32_t(32 * (warp % 4)) << 16);
-    const uint32_t scol = tlane + kScol + 128 * tile, ocol = tlane + kOcol + 128 * tile;
+    const uint32_t ocol = tlane + kOcol + 128 * tile;
 
     // ---- the warp's 32 query rows to shared memory, a row at a time across the lanes: with
     // sm_scale's sign, binary16 (bfloat16 rows scaled by a power of two so that the largest value
     // fits: what is lost below is under 2^-25 of it)
     const int steps = t.steps_of[tile];
     const uint32_t lives = __ballot_sync(0xffffffffu, live);
-    const int d4 = 4 * lane;  // the lane's four values of a row
+    const int d4 = 4 * lane;  // the lane's four values of a row (or of each of its halves)
     uint8_t *rows_sm = qsm + tile * Layout<DT>::kQ + 32 * (warp % 4) * 128;
     float unscale = 1.f;
-    constexpr int kBatch = 8;  // rows whose loads are in flight together
+    constexpr int kBatch = 8 / kBoxes;  // rows whose loads are in flight together
 #pragma unroll 1
     for (int r0 = 0; r0 < 32; r0 += kBatch) {
-        uint2 x[kBatch];
+        uint2 x[kBatch][kBoxes];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int64_t from = __shfl_sync(0xffffffffu, at, r0 + k);
-            x[k] = (lives >> (r0 + k) & 1) && d4 < a.head_dim
-                       ? *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + from + d4) : make_uint2(0, 0);
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c)
+                x[k][c] = (lives >> (r0 + k) & 1) && d4 + 128 * c < a.head_dim
+                              ? *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + from + d4 + 128 * c)
+                              : make_uint2(0, 0);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if constexpr (BF16) {
-                const float2 lo = act_f2<T>(x[k].x), hi = act_f2<T>(x[k].y);
-                const float amax = __uint_as_float(warp_umax(__float_as_uint(
-                    fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y))))));
+                float amax = 0.f;
+#pragma unroll
+                for (int c = 0; c < kBoxes; ++c) {
+                    const float2 lo = act_f2<T>(x[k][c].x), hi = act_f2<T>(x[k][c].y);
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(lo.x), fabsf(lo.y)), fmaxf(fabsf(hi.x), fabsf(hi.y))));
+                }
+                amax = __uint_as_float(warp_umax(__float_as_uint(amax)));
                 const int e = kv_clamp(int(__float_as_uint(amax) >> 23) - 127, -120, 120);
                 const float up = copysignf(__uint_as_float(uint32_t(127 - e) << 23), a.sm_scale);
                 if (lane == r0 + k) unscale = __uint_as_float(uint32_t(127 + e) << 23);
-                x[k] = make_uint2(act_t2<__half>(lo.x * up, lo.y * up), act_t2<__half>(hi.x * up, hi.y * up));
+#pragma unroll
+                for (int c = 0; c < kBoxes; ++c) {
+                    const float2 lo = act_f2<T>(x[k][c].x), hi = act_f2<T>(x[k][c].y);
+                    x[k][c] = make_uint2(act_t2<__half>(lo.x * up, lo.y * up), act_t2<__half>(hi.x * up, hi.y * up));
+                }
             } else if (a.sm_scale < 0.f) {
-                x[k].x ^= 0x80008000u;
-                x[k].y ^= 0x80008000u;
+#pragma unroll
+                for (int c = 0; c < kBoxes; ++c) {
+                    x[k][c].x ^= 0x80008000u;
+                    x[k][c].y ^= 0x80008000u;
+                }
             }
-            if (d4 < DT) {
-                uint8_t *p = rows_sm + d4 / 64 * Layout<DT>::kAtom + (r0 + k) * 128 + (((d4 % 64 / 8) ^ (k & 7)) << 4) + d4 % 8 * 2;
-                *reinterpret_cast<uint2 *>(p) = x[k];
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c) {
+                const int d = d4 + 128 * c;
+                if (d < DT)
+                    *reinterpret_cast<uint2 *>(rows_sm + d / 64 * L::kAtom + (r0 + k) * 128 +
+                                               (((d % 64 / 8) ^ ((r0 + k) & 7)) << 4) + d % 8 * 2) = x[k][c];
             }
         }
     }
@@ -554,7 +616,9 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
     float m = -INFINITY, l = 0.f, vref = 0.f;
     for (int j = 0; j < steps; ++j) {
         const int set = j % kRing, key0 = j * kKeys;
-        if (!wait_warp(&bar.sc_full[set], (j / kRing) & 1, abort) || !wait_warp(&bar.s_full[tile], j & 1, abort)) return;
+        const uint32_t scol = tlane + kScol + L::kSCols * L::slot(tile, j);
+        if (!wait_warp(&bar.sc_full[set], (j / kRing) & 1, abort) ||
+            !wait_warp(&bar.s_full[L::slot(tile, j)], L::parity(j), abort)) return;
         tc::fence_after_sync();
         const int left = seen - key0;  // keys of this step that the row sees
         const int least = __reduce_min_sync(0xffffffffu, left);
@@ -572,23 +636,26 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
             if (refer && !new_references<DT>(scol, ocol, sc, set, unscale, left, all_seen && !dead, dead, j, tile, bar, abort, m, vref, l))
                 return;
             if (!plain) {
-                weights_any(scol, sc, set, unscale, left, dead, m, vref, l);
+                weights_any<kGroups>(scol, sc, set, unscale, left, dead, m, vref, l);
                 break;
             }
             const float shift = kRaise - (m == -INFINITY ? 0.f : m) - float(int(__float_as_uint(vref) >> 23) - 127);
             float lsum = 0.f;
             const bool fits = all_seen
-                                  ? weights_once<false>(scol, sc.k[set], sc.log_v[set], sc.inv_v[set], unscale, shift, left, lsum, refer)
-                                  : weights_once<true>(scol, sc.k[set], sc.log_v[set], sc.inv_v[set], unscale, shift, left, lsum, refer);
+                                  ? weights_once<false, kGroups>(scol, sc.k[set], sc.log_v[set], sc.inv_v[set], unscale, shift, left, lsum, refer)
+                                  : weights_once<true, kGroups>(scol, sc.k[set], sc.log_v[set], sc.inv_v[set], unscale, shift, left, lsum, refer);
             if (fits) {
                 l = fmaf(lsum, vref, l);
                 break;
             }
             refer = true;
         }
+        // One tile: the sums of the step before need not be done yet.  They run before this step's anyway;
+        // waited for here, the barrier is never two phases behind a wait.
+        if (!L::kTwo && j > 0 && !wait_warp(&bar.o_done[tile], (j - 1) & 1, abort)) return;
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[tile]);
+        if (lane == 0) mbar_arrive(&bar.p_full[L::slot(tile, j)]);
     }
     if (steps > 0 && !wait_warp(&bar.o_done[tile], (steps - 1) & 1, abort)) return;
     tc::fence_after_sync();
@@ -620,9 +687,13 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
 #pragma unroll 8
     for (int k = 0; k < 32; ++k) {
         const int64_t to = __shfl_sync(0xffffffffu, at, k);
-        if ((lives >> k & 1) && d4 < a.head_dim)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to + d4) =
-                lds64(back + k * (2 * DT) + (((d4 / 8) ^ (k & 7)) << 4) + d4 % 8 * 2);
+#pragma unroll
+        for (int c = 0; c < kBoxes; ++c) {
+            const int d = d4 + 128 * c;
+            if ((lives >> k & 1) && d < a.head_dim)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to + d) =
+                    lds64(back + k * (2 * DT) + (((d / 8) ^ (k & 7)) << 4) + d % 8 * 2);
+        }
     }
 }
 
@@ -631,14 +702,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                      const __grid_constant__ KvAttnArgs a)
 {
+    using L = Layout<DT>;
+    constexpr int kRows = L::kRows, kKeys = L::kKeys;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Bars bar;
     __shared__ Scales sc;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, s_seq[4];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *qsm = smem, *ksm = qsm + 2 * Layout<DT>::kQ, *vsm = ksm + 2 * Layout<DT>::kQ;
-    uint8_t *kraw = vsm + 2 * Layout<DT>::kV, *vraw = kraw + Layout<DT>::kRaw;
+    uint8_t *qsm = smem, *ksm = qsm + kRows / kTile * L::kQ, *vsm = ksm + 2 * L::kK;
+    uint8_t *kraw = vsm + 2 * L::kV, *vraw = kraw + L::kRaw;
     volatile int *abort = &abort_flag;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
@@ -682,8 +755,8 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     if (tid == 0) {
         mbar_init(&bar.q_full, 4 * t.tiles);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.k_full[i], kConvWarps);
-            mbar_init(&bar.v_full[i], kConvWarps);
+            mbar_init(&bar.k_full[i], L::kConvWarps);
+            mbar_init(&bar.v_full[i], L::kConvWarps);
             mbar_init(&bar.k_free[i], 1);
             mbar_init(&bar.v_free[i], 1);
             mbar_init(&bar.s_full[i], 1);
@@ -693,8 +766,8 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
         for (int i = 0; i < kRing; ++i) mbar_init(&bar.sc_full[i], 1);
         mbar_init(&bar.raw_k_full, 1);
         mbar_init(&bar.raw_v_full, 1);
-        mbar_init(&bar.raw_k_free, kConvWarps);
-        mbar_init(&bar.raw_v_free, kConvWarps);
+        mbar_init(&bar.raw_k_free, L::kConvWarps);
+        mbar_init(&bar.raw_v_free, L::kConvWarps);
         mbar_init(&bar.fin, 1);
         fence_barrier_init();
         tma_prefetch_desc(&km);
@@ -712,13 +785,13 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     grid_dep_launch();
     const uint32_t tbase = tmem_slot;
 
-    if (warp < kSoftWarps) {
+    if (warp < L::kSoftWarps) {
         softmax_role<BF16, DT>(a, t, qsm, sc, bar, tbase, abort);
     } else if (t.steps > 0) {
         if (warp < kMmaWarp)
             convert_role<F8, DT>(a, t, kraw, vraw, ksm, vsm, sc, bar, abort);
         else if (warp == kCopyWarp)
-            copy_role(a, t, &km, &vm, kraw, vraw, sc, bar, abort);
+            copy_role<DT>(a, t, &km, &vm, kraw, vraw, sc, bar, abort);
         else if (lane == 0)
             mma_role<DT>(a, t, smem_u32(qsm), smem_u32(ksm), smem_u32(vsm), bar, tbase, abort);
     }
@@ -729,31 +802,39 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     if (warp == kMmaWarp) tc::tmem_dealloc(tbase, kTmemCols);
 }
 
-template <bool F8, bool BF16>
-const void *tiles_kernel(bool small)
+struct TilesPlan {
+    const void *fn;
+    int rows, keys, smem;
+};
+
+template <bool F8, bool BF16, int DT>
+TilesPlan tiles_plan()
 {
-    return small ? reinterpret_cast<const void *>(kv_attn_tiles_kernel<F8, BF16, 64>)
-                 : reinterpret_cast<const void *>(kv_attn_tiles_kernel<F8, BF16, 128>);
+    return {reinterpret_cast<const void *>(kv_attn_tiles_kernel<F8, BF16, DT>), Layout<DT>::kRows, Layout<DT>::kKeys,
+            Layout<DT>::kBytes + 1024};
+}
+
+template <bool F8, bool BF16>
+TilesPlan tiles_plan(int head_dim)
+{
+    return head_dim <= 64 ? tiles_plan<F8, BF16, 64>() : head_dim <= 128 ? tiles_plan<F8, BF16, 128>() : tiles_plan<F8, BF16, 256>();
 }
 
 }  // namespace
 
 wq_status kv_attn_tiles(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
 {
-    const bool small = a.head_dim <= 64;
-    const void *fn = f8 ? (bf16 ? tiles_kernel<true, true>(small) : tiles_kernel<true, false>(small))
-                        : (bf16 ? tiles_kernel<false, true>(small) : tiles_kernel<false, false>(small));
-    // the most that any sequence of the call leaves for its Tensor Memory: one block an SM
-    const int smem = 1024 + (small ? Layout<64>::kBytes : Layout<128>::kBytes);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    const TilesPlan p = f8 ? (bf16 ? tiles_plan<true, true>(a.head_dim) : tiles_plan<true, false>(a.head_dim))
+                           : (bf16 ? tiles_plan<false, true>(a.head_dim) : tiles_plan<false, false>(a.head_dim));
+    if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_tiles_kernel)");
-    const int64_t blocks = kv_row_item(a.M, a.n_seqs, a.group, kRows) * a.kv_heads;
+    const int64_t blocks = kv_row_item(a.M, a.n_seqs, a.group, p.rows) * a.kv_heads;
     if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
     CUtensorMap km, vm;
-    wq_status rc = encode_cache(&km, &vm, a, std::min(1 << a.page_shift, kKeys));
+    wq_status rc = encode_cache(&km, &vm, a, std::min(1 << a.page_shift, p.keys));
     if (rc != WQ_OK) return rc;
     PreparedLaunch L;
-    set_attn_launch(L, fn, unsigned(blocks), kThreads, size_t(smem), km, vm, a);
+    set_attn_launch(L, p.fn, unsigned(blocks), kThreads, size_t(p.smem), km, vm, a);
     return launch_prepared(L, st, "kv_attn_tiles_kernel");
 }
 

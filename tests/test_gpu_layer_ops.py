@@ -370,6 +370,8 @@ ATTEND = [
     ([130, 1, 17], [200, 500, 17], 4, 1, 64, 256),
     ([1] * 9, [1, 2, 3, 31, 32, 33, 400, 64, 65], 2, 2, 20, 32),
     ([67], [67], 3, 1, 52, 16),
+    ([1, 1, 1, 1, 1], [5, 300, 64, 1000, 17], 2, 1, 256, 32),  # one row of a head above 128
+    ([2, 1, 3, 1], [40, 300, 3, 129], 4, 2, 192, 16),
 ]
 
 
@@ -422,6 +424,12 @@ def test_attention_scores_of_any_size():
         _attend_check(s, q, _attend(s, q, cache, batch, sm_scale=sm), sm)
 
 
+def _many(new, q_heads, kv_heads):
+    """(q_heads, kv_heads) in the same ratio with more rows in all than the split by keys takes."""
+    f = -(-3600 // (sum(new) * q_heads))
+    return f * q_heads, f * kv_heads
+
+
 TILES = [
     ([300], [300], 4, 2, 128, 16),                             # three blocks of 256 rows, causal
     ([200, 3, 129], [900, 200, 129], 4, 2, 128, 64),           # long past; a sequence of few rows among them
@@ -430,6 +438,11 @@ TILES = [
     ([90, 45], [333, 45], 5, 1, 100, 32),
     ([70], [1500], 8, 1, 48, 256),
     ([100, 100], [100, 0], 3, 3, 112, 16),                     # all rows without keys
+    ([300], [300], 4, 2, 256, 64),                             # heads above 128: blocks of 128 rows
+    ([200, 3, 129], [900, 200, 129], 2, 1, 192, 16),
+    ([40, 1, 0, 90], [700, 333, 90, 91], 4, 1, 132, 128),
+    ([140, 60], [100, 60], 2, 1, 256, 256),
+    ([100, 65], [0, 65], 3, 3, 160, 32),
 ]
 
 
@@ -437,6 +450,7 @@ TILES = [
 @pytest.mark.parametrize("case", TILES, ids=lambda c: "q%s_h%d-%d_d%d_p%d" % ("-".join(map(str, c[0])), c[2], c[3], c[4], c[5]))
 def test_attention_many_rows(case, dtype, out):
     new, total, hq, hkv, D, page = case
+    hq, hkv = _many(new, hq, hkv)
     s = Setup(new, total, hq, hkv, D, page, dtype, out, seed=sum(total) + D, tail=3).fill(total)
     cache, batch = s.device()
     q = s.q()
@@ -445,11 +459,12 @@ def test_attention_many_rows(case, dtype, out):
     assert torch.equal(_attend(s, q, cache, batch), got)
 
 
+@pytest.mark.parametrize("D", [128, 200])
 @pytest.mark.parametrize("out", ["int8", "fp8"])
-def test_attention_many_rows_uneven(out):
+def test_attention_many_rows_uneven(out, D):
     """Value scales and scores that rise by orders of magnitude along the keys and fall again: the running
     references move often."""
-    s = Setup([150], [700], 2, 1, 128, 16, "fp16", out, seed=31).fill([700])
+    s = Setup([150], [700], *_many([150], 2, 1), D, 16, "fp16", out, seed=31).fill([700])
     order = s.table[0, : -(-700 // 16)]
     rise = np.concatenate([np.linspace(-4, 0, 30), np.linspace(0, -5, order.size - 30)])
     s.host.vs[order, 0] = (10.0 ** rise * 0.03).astype(np.float32)
@@ -459,8 +474,9 @@ def test_attention_many_rows_uneven(out):
     _attend_check(s, q, _attend(s, q, cache, batch))
 
 
-def test_attention_many_rows_with_a_bad_page():
-    s = Setup([60, 60], [300, 300], 2, 1, 128, 16, "bf16", "fp8", seed=33).fill([300, 300])
+@pytest.mark.parametrize("D", [128, 256])
+def test_attention_many_rows_with_a_bad_page(D):
+    s = Setup([60, 60], [300, 300], *_many([120], 2, 1), D, 16, "bf16", "fp8", seed=33).fill([300, 300])
     s.table[0, 4] = -7
     cache, batch = s.device()
     q = s.q()
@@ -468,6 +484,17 @@ def test_attention_many_rows_with_a_bad_page():
     torch.cuda.synchronize()
     assert wq.device_error() == 3
     _attend_check(s, q, got)
+
+
+@pytest.mark.parametrize("D,new,heads", [(128, 1, 1), (256, 1, 1), (256, 1, 12), (64, 1, 2)])
+def test_attention_most_sequences(D, new, heads):
+    """4096 sequences, the most of a call, in each kernel for few rows."""
+    r = np.random.default_rng(8)
+    total = [int(x) for x in r.integers(0, 20, 4096)]
+    s = Setup([new] * 4096, total, heads, 1, D, 16, "bf16", "int8", seed=D).fill(total)
+    cache, batch = s.device()
+    q = s.q()
+    _attend_check(s, q, _attend(s, q, cache, batch))
 
 
 def test_attention_many_sequences():
@@ -597,7 +624,7 @@ def test_attention_of_two_streams_at_once():
     """Few and many rows, each with a workspace of its own, beside each other: the bits of one
     after the other."""
     few = Setup([1] * 6, [3000, 1, 700, 2500, 64, 900], 8, 2, 64, 32, "bf16", "fp8", seed=3).fill([3000, 1, 700, 2500, 64, 900])
-    many = Setup([300, 1, 90], [900, 2000, 90], 8, 1, 64, 64, "fp16", "int8", seed=4).fill([900, 2000, 90])
+    many = Setup([300, 1, 90], [900, 2000, 90], 16, 2, 64, 64, "fp16", "int8", seed=4).fill([900, 2000, 90])
     runs = []
     for s in (few, many):
         cache, batch = s.device()
