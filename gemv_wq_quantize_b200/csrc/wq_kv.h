@@ -36,11 +36,17 @@ WQ_HD KvSpan kv_span(int cu_lo, int cu_hi, int seq_len, int M, int capacity)
     return s;
 }
 
-// The work items of an append are (sequence, page): sequence b owns the items from
-// kv_item_start(q0_b, b) to kv_item_start(q0_{b+1}, b + 1), at least floor(n / page) + 2 of
-// them, and n tokens touch at most floor((n + page - 2) / page) + 1 pages.  So an item's
-// sequence follows from cu_q alone, without a sum over the sequences before it.
-WQ_HD int64_t kv_item_start(int q0, int b, int page_shift) { return int64_t(q0 >> page_shift) + 2 * int64_t(b); }
+// An append's work: a sequence with up to kKvFewTokens tokens in the call is one item, and the
+// others' items are (sequence, page): sequence b with tokens q0 .. q1 - 1 owns those from
+// kv_item_start(q0, b) to kv_item_start(q1, b + 1), at least floor(n / page) + 2 of them (floor(n / 4)
+// is at least 2), and n tokens touch at most floor((n + page - 2) / page) + 1 pages.  So an item's
+// sequence follows from cu_q alone, without a sum over the sequences before it.  by_seq: two items a
+// sequence beside the pages, else one for every four tokens: whichever makes fewer.
+constexpr int kKvFewTokens = 8;
+WQ_HD int64_t kv_item_start(int q0, int b, int page_shift, bool by_seq)
+{
+    return int64_t(q0 >> page_shift) + (by_seq ? 2 * int64_t(b) : int64_t(q0 >> 2));
+}
 
 // Item k of a sequence: the logical page and the call's tokens in it.
 struct KvPageSpan {

@@ -8,13 +8,19 @@
 //
 // Work items.  The maximum over a page's new tokens needs one owner per (page, head): a block
 // owns one (sequence, page) item and a head's keys or values; which sequence an item belongs to
-// follows from cu_q alone (wq_kv.h), found by all threads of the block looking at once.  Where
-// sequences bring few tokens, a block owns a sequence and four heads, a warp for each.  A group of WPT
+// follows from cu_q alone (wq_kv.h), found by all threads of the block looking at once.  For a
+// sequence of few tokens a block owns the sequence and four heads, a warp for each's keys or
+// values.  A group of WPT
 // warps owns the keys or the values of one head: every lane holds four neighbouring values of a
 // row (so the partner of a rotated value is one more 8-byte load of the same row, not a
 // shuffle), the rows of the page go over the group's warps, and the rotated values stay in
 // registers between the maximum and the codes.  Other blocks of the same launch turn the
 // queries.
+//
+// Bound by instruction issue for long runs (rotation, codes), else by the launch and the chain of
+// table, row, maximum and codes.  Measured, 32 query heads: 8192 tokens in six runs, 8 key heads of
+// 128: 38 us, 3.2 TB/s (108 us with branches around the loads and a division a code); 48 sequences of
+// 1 to 6 tokens, 32 key heads of 100: 8.1 us; 16 of one token, 32 key heads of 128: 3.6 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -60,8 +66,9 @@ struct AppendArgs {
     int capacity;       // tokens that the block table's row holds
     int limit;          // positions below it have a place: min(capacity, rope_len)
     bool pairs;         // WQ_ROPE_PAIRS
-    int64_t kv_items;   // (sequence, page) items, or sequences (few tokens each)
-    int parts;          // blocks per item
+    int items;          // (sequence, page) items of long runs
+    int run_blocks;     // and the blocks that take them
+    int parts;          // blocks of a sequence of few tokens
     int q_tokens;       // tokens of a query block
 };
 
@@ -207,8 +214,10 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, const T *src, c
 {
     constexpr int kHeld = kHeldFloats / (4 * CH);
     // Rows whose loads are in flight together.  A warp that has a page to itself mostly holds one or
-    // two rows: more at once is code to step over (few tokens: 9.6 us with 4, 7.7 with 1).
-    constexpr int kBatch = WPT == 1 ? 1 : kHeld < 8 ? kHeld : 8;
+    // two rows: more at once is code to step over (few tokens: 9.6 us with 4, 7.7 with 1).  A row that
+    // turns by halves has two loads and a table of its own a lane: more than 2 spill (4096 tokens 36.8
+    // us, with 8 40.3; turned by pairs 39.5 and 37.8).
+    constexpr int kMost = WPT == 1 ? 1 : MODE == kPairs || MODE == kNone ? 8 : 2, kBatch = kHeld < kMost ? kHeld : kMost;
     const int lane = threadIdx.x % 32, D = a.c.head_dim;
     const int64_t row_stride = int64_t(a.q_heads + 2 * a.c.kv_heads) * D;
     auto dim = [&](int c) { return 4 * (lane + 32 * c); };
@@ -333,42 +342,52 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int b, int seq_
         append_rows<T, F8, WPT, CH, kNone>(a, src, nullptr, ps, count, live, scale, codes, wi, s_max);
 }
 
-// WPT > 1: a (sequence, page) item.  WPT 1 (few tokens a sequence): all pages of sequence `item`.
-template <typename T, bool F8, int WPT, int CH, Mode MODE>
-__device__ __forceinline__ void append_item(const AppendArgs &a, int64_t item, int part)
+// All pages of a sequence of few tokens, a warp for the keys or the values of a head.
+template <typename T, bool F8, int CH, Mode MODE>
+__device__ __forceinline__ void append_few(const AppendArgs &a, int b, int part)
+{
+    const int len = __ldg(a.seq_len + b);
+    const KvSpan span = kv_span(__ldg(a.cu_q + b), __ldg(a.cu_q + b + 1), len, a.M, a.capacity);
+    if (span.n > kKvFewTokens) return;
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+        const KvPageSpan ps = kv_page_span(span, k, a.page_shift);
+        if (ps.count == 0) break;
+        append_page<T, F8, 1, CH, MODE>(a, b, len, ps, part, nullptr);
+    }
+}
+
+// A (sequence, page) item of a long run, all warps for the keys or the values of a head.  False: the
+// call has no long run.
+template <typename T, bool F8, int CH, Mode MODE, bool RUNS>
+__device__ __forceinline__ bool append_item(const AppendArgs &a, int item, int part)
 {
     __shared__ float s_max[kWarps];
-    if constexpr (WPT == 1) {
-        const int b = int(item), len = __ldg(a.seq_len + b);
-        const KvSpan span = kv_span(__ldg(a.cu_q + b), __ldg(a.cu_q + b + 1), len, a.M, a.capacity);
-#pragma unroll 1
-        for (int k = 0;; ++k) {
-            const KvPageSpan ps = kv_page_span(span, k, a.page_shift);
-            if (ps.count == 0) break;
-            append_page<T, F8, WPT, CH, MODE>(a, b, len, ps, part, s_max);
+    __shared__ int s_seq[4];
+    const int tid = threadIdx.x;
+    if (tid == 0) s_seq[0] = -1;
+    __syncthreads();
+    bool any = false;
+    for (int b = tid; b < a.n_seqs; b += kThreads) {
+        const int lo = a.cu_q[b], hi = a.cu_q[b + 1];
+        const int q0 = kv_clamp(lo, 0, a.M), q1 = kv_clamp(hi, q0, a.M);
+        if (q1 - q0 <= kKvFewTokens) continue;
+        any = true;
+        if (kv_item_start(q0, b, a.page_shift, RUNS) <= item && item < kv_item_start(q1, b + 1, a.page_shift, RUNS)) {
+            s_seq[0] = b;
+            s_seq[1] = lo;
+            s_seq[2] = hi;
+            s_seq[3] = a.seq_len[b];
         }
-    } else {
-        __shared__ int s_seq[4];
-        const int tid = threadIdx.x;
-        if (tid == 0) s_seq[0] = -1;
-        __syncthreads();
-        for (int b = tid; b < a.n_seqs; b += kThreads) {
-            const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
-            const int q0 = kv_clamp(lo, 0, a.M), q1 = kv_clamp(hi, q0, a.M);
-            if (kv_item_start(q0, b, a.page_shift) <= item && item < kv_item_start(q1, b + 1, a.page_shift)) {
-                s_seq[0] = b;
-                s_seq[1] = lo;
-                s_seq[2] = hi;
-                s_seq[3] = len;
-            }
-        }
-        __syncthreads();
-        const int b = s_seq[0];
-        if (b < 0) return;
-        const KvSpan span = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
-        const KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift), a.page_shift);
-        if (ps.count) append_page<T, F8, WPT, CH, MODE>(a, b, s_seq[3], ps, part, s_max);
     }
+    if (!__syncthreads_or(any)) return false;
+    const int b = s_seq[0];
+    if (b >= 0) {
+        const KvSpan span = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
+        const KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift, RUNS), a.page_shift);
+        if (ps.count) append_page<T, F8, kWarps, CH, MODE>(a, b, s_seq[3], ps, part, s_max);
+    }
+    return true;
 }
 
 // The queries of q_tokens tokens: kWarps / q_tokens warps take a token's heads in turn.
@@ -425,37 +444,52 @@ __device__ __forceinline__ void turn_queries(const AppendArgs &a, int64_t block)
     }
 }
 
-template <typename T, bool F8, int WPT, int CH, Mode MODE>
+// RUNS: many tokens a sequence on average, and a block for each item and head of the long runs.  Else
+// there mostly is no long run, so a few blocks look and, if there is one, take its items in turn.
+template <typename T, bool F8, int CH, Mode MODE, bool RUNS>
 __global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : 2) kv_append_kernel(const __grid_constant__ AppendArgs a)
 {
     grid_dep_launch();
     grid_dep_wait();  // the QKV projection and the batch's arrays may come from the kernel before
-    const int64_t kv_blocks = a.kv_items * a.parts;
-    if (int64_t(blockIdx.x) < kv_blocks)
-        append_item<T, F8, WPT, CH, MODE>(a, blockIdx.x / a.parts, blockIdx.x % a.parts);
-    else
-        turn_queries<T, CH, MODE>(a, blockIdx.x - kv_blocks);
+    // pages of long runs first, which take longest
+    const int few_blocks = a.n_seqs * a.parts, pairs = 2 * a.c.kv_heads;
+    int block = blockIdx.x;
+    if (block < a.run_blocks) {
+        if constexpr (RUNS) {
+            append_item<T, F8, CH, MODE, RUNS>(a, block / pairs, block % pairs);
+        } else {
+#pragma unroll 1
+            for (; block < a.items * pairs; block += a.run_blocks) {
+                if (!append_item<T, F8, CH, MODE, RUNS>(a, block / pairs, block % pairs)) break;
+                __syncthreads();  // the block's shared memory is read
+            }
+        }
+        return;
+    }
+    block -= a.run_blocks;
+    if (block < few_blocks) append_few<T, F8, CH, MODE>(a, block / a.parts, block % a.parts);
+    else turn_queries<T, CH, MODE>(a, block - few_blocks);
 }
 
 template <typename T, bool F8, Mode MODE>
-const void *append_kernel(bool many, bool wide)
+const void *append_kernel(bool wide, bool runs)
 {
-    if (many)
-        return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, kWarps, 2, MODE>)
-                    : reinterpret_cast<const void *>(kv_append_kernel<T, F8, kWarps, 1, MODE>);
-    return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, 2, MODE>)
-                : reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, 1, MODE>);
+    if (runs)
+        return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, 2, MODE, true>)
+                    : reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, MODE, true>);
+    return wide ? reinterpret_cast<const void *>(kv_append_kernel<T, F8, 2, MODE, false>)
+                : reinterpret_cast<const void *>(kv_append_kernel<T, F8, 1, MODE, false>);
 }
 
 template <typename T, bool F8>
-const void *append_kernel(Mode mode, bool many, bool wide)
+const void *append_kernel(Mode mode, bool wide, bool runs)
 {
     switch (mode) {
-    case kNone: return append_kernel<T, F8, kNone>(many, wide);
-    case kPairs: return append_kernel<T, F8, kPairs>(many, wide);
-    case kHalf: return append_kernel<T, F8, kHalf>(many, wide);
-    case kHalf2: return append_kernel<T, F8, kHalf2>(many, wide);
-    default: return append_kernel<T, F8, kAny>(many, wide);
+    case kNone: return append_kernel<T, F8, kNone>(wide, runs);
+    case kPairs: return append_kernel<T, F8, kPairs>(wide, runs);
+    case kHalf: return append_kernel<T, F8, kHalf>(wide, runs);
+    case kHalf2: return append_kernel<T, F8, kHalf2>(wide, runs);
+    default: return append_kernel<T, F8, kAny>(wide, runs);
     }
 }
 
@@ -534,18 +568,27 @@ extern "C" wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t 
                       : a.pairs                           ? (rope_dim % 4 == 0 ? kPairs : kAny)
                       : rope_dim % 8 == 0 ? kHalf
                       : rope_dim % 4 == 0 ? kHalf2 : kAny;
-    // A page's rows go over all warps of a block where sequences bring many tokens, else one warp
-    // takes each (head, keys or values).
-    const bool many = M >= 4 * batch->n_seqs;
-    a.parts = many ? 2 * cache->kv_heads : (2 * cache->kv_heads + kWarps - 1) / kWarps;
-    a.kv_items = many ? (M >> a.page_shift) + 2 * batch->n_seqs : batch->n_seqs;
-    a.q_tokens = M <= 1024 ? 1 : kWarps;
-    const int64_t blocks = a.kv_items * a.parts + (M + a.q_tokens - 1) / a.q_tokens;
-    if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
+    // A page's rows go over all warps of a block for sequences that bring many tokens, else one warp
+    // takes each (head, keys or values): 32 sequences of 8 tokens, 8 key heads, 7.1 us against 11.4 of
+    // the former; 8 sequences of 16 tokens 12.1 against 4.9.
+    a.parts = (2 * cache->kv_heads + kWarps - 1) / kWarps;
+    // (a block an item with few tokens a sequence: 48 sequences of 1 to 6 tokens, 32 key heads, 12.3 us
+    // instead of 8.1; one run of 380 tokens beside 127 of one: 18 us, 285 by a warp each)
+    const bool runs = M > kKvFewTokens * batch->n_seqs;
+    const int64_t items = M > kKvFewTokens ? kv_item_start(int(M), int(batch->n_seqs), a.page_shift, runs) : 0;
+    const int64_t all = items * 2 * cache->kv_heads, run_blocks = runs ? all : std::min<int64_t>(all, device_info().sm_count);
+    // Queries, a block a token or a warp a token: 1024 tokens of 32 heads 13.2 / 14.5 us, 1600 19.2 /
+    // 19.5, 4096 48.5 / 39.3.
+    a.q_tokens = M <= 1600 ? 1 : kWarps;
+    const int64_t blocks = run_blocks + batch->n_seqs * a.parts + (M + a.q_tokens - 1) / a.q_tokens;
+    if (std::max(all, blocks) > 0x7fffffff - device_info().sm_count)
+        return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
+    a.items = int(items);
+    a.run_blocks = int(run_blocks);
     const bool wide = cache->head_dim > 128, f8 = cache->format == WQ_FMT_E4M3;
-    const void *fn = dt == WQ_F16 ? (f8 ? append_kernel<__half, true>(mode, many, wide) : append_kernel<__half, false>(mode, many, wide))
-                                  : (f8 ? append_kernel<__nv_bfloat16, true>(mode, many, wide)
-                                        : append_kernel<__nv_bfloat16, false>(mode, many, wide));
+    const void *fn = dt == WQ_F16 ? (f8 ? append_kernel<__half, true>(mode, wide, runs) : append_kernel<__half, false>(mode, wide, runs))
+                                  : (f8 ? append_kernel<__nv_bfloat16, true>(mode, wide, runs)
+                                        : append_kernel<__nv_bfloat16, false>(mode, wide, runs));
     PreparedLaunch L;
     L.set(fn, dim3(unsigned(blocks)), dim3(kThreads), 0, a);
     return launch_prepared(L, stream, "kv_append_kernel");

@@ -24,11 +24,17 @@
 //  * warp 5: fills a ring of stages of 128 keys and values by TMA, page by page, and their scales.
 // Every wait is bounded; on expiry the block records an error, stops and frees its Tensor Memory.
 //
-// Work split: tiles (sequence, key head, 8 or 16 rows) are cut into units of 128 keys, and the
+// Work split: tiles (sequence, key head, 8 rows) are cut into units of 128 keys, and the
 // persistent blocks take equal contiguous shares of all units, whatever the lengths (a tile counts
 // kTileUnits more, about what its start and end take).  A tile cut over several blocks leaves
 // partial sums in the workspace; the last block to arrive adds them in the order of their keys,
 // so the result does not depend on which block that is.
+//
+// Measured, 32 query heads: two sequences of 131000 keys, 8 key heads of 128: 93 us, 5.8 TB/s;
+// 32 of 100 to 4095 keys: 42 us, 3.2 TB/s; 16 of 2 to 6 tokens and 300 to 2000 keys, 32 key heads
+// of 100: 52 us, 2.0 TB/s; one of 512 keys, 32 key heads: 14 us, where a block's start (Tensor
+// Memory, shares, queries), one step and the joining of the parts follow one another.  Against
+// codes widened in registers (mma.sync, per-warp rings): 114, 43, 48 and 13 us.
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -62,7 +68,7 @@ constexpr int kMmaWarp = 4, kCopyWarp = 5, kThreads = 192;
 constexpr int kParts = 4;                // 8-bit parts of a query value or weight
 constexpr int kUnitShift = 7;            // a unit: 128 keys, the granule of the split
 constexpr int kTileUnits = 4;            // what the start and end of a tile cost a block, in units
-constexpr int kLeastUnits = 1;           // of a share: less only adds partials
+constexpr int kLeastUnits = 1;           // of a share, beside them: more leaves SMs idle at short lengths
 constexpr int kMostUnits = 0x7fffff00;   // of a call
 
 __device__ __forceinline__ uint64_t globaltimer()
@@ -72,13 +78,18 @@ __device__ __forceinline__ uint64_t globaltimer()
     return t;
 }
 
+// Rows of a tile.  16 (and a stage less in the ring) measured slower even where a sequence has more, whose
+// keys are then read again from L2: 16 sequences of 2000 keys and 16 rows 43 / 50 us, two of 8000 keys
+// and 96 rows 71 / 78.
+constexpr int kRowsOfTile = 8;
+
 // NB: boxes of 128 dimensions (1 up to a head size of 128, 2 up to 256).  NR: rows of a tile.
 template <int NB, int NR>
 struct Shape {
     static constexpr int kN = kParts * NR;               // MMA N
     static constexpr int kBox = kKeys * 128;             // bytes of 128 keys x 128 dimensions
     static constexpr int kPerSm = NB == 1 ? 2 : 1;       // blocks
-    static constexpr int kStages = NR == 8 ? 3 : 2;      // 96 KB (64 KB) of a block's share of an SM
+    static constexpr int kStages = 3;                    // 96 KB (192 KB) of a block's share of an SM
     static constexpr int kRowFloats = 128 * NB + 4;      // a partial row: sums, maximum, weight sum
     static constexpr uint32_t kSCol = 0, kOCol = 2 * kN; // two of each: scores [2], sums [2][NB]
     static constexpr uint32_t kUsed = 2 * kN * (1 + NB), kTmem = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
@@ -926,17 +937,16 @@ RowsPlan rows_plan()
 }
 
 template <bool F8, bool BF16>
-RowsPlan rows_plan(int head_dim, bool two)
+RowsPlan rows_plan(int head_dim)
 {
-    if (head_dim <= 128) return two ? rows_plan<F8, BF16, 1, 16>() : rows_plan<F8, BF16, 1, 8>();
-    return two ? rows_plan<F8, BF16, 2, 16>() : rows_plan<F8, BF16, 2, 8>();
+    return head_dim <= 128 ? rows_plan<F8, BF16, 1, kRowsOfTile>() : rows_plan<F8, BF16, 2, kRowsOfTile>();
 }
 
 constexpr int kMostPerSm = 2;
 constexpr int kFewRows = 16;
-// two partial slots a block in the workspace's 64 KB per SM: two blocks of 16 rows of 132 binary32
-// values, or one of 16 rows of 260
-static_assert(2 * 2 * 16 * (128 + 4) * 4 <= 65536 && 2 * 16 * (256 + 4) * 4 <= 65536, "");
+// two partial slots a block in the workspace's 64 KB per SM: two blocks of 8 rows of 132 binary32
+// values, or one of 8 rows of 260
+static_assert(2 * 2 * kRowsOfTile * (128 + 4) * 4 <= 65536 && 2 * kRowsOfTile * (256 + 4) * 4 <= 65536, "");
 
 }  // namespace
 
@@ -974,10 +984,8 @@ void set_attn_launch(PreparedLaunch &L, const void *fn, unsigned blocks, int thr
 
 wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
 {
-    // 16 rows a tile where sequences bring more than 8 rows per key head on average
-    const bool two = int64_t(a.M) * a.group > int64_t(8) * a.n_seqs;
-    const RowsPlan p = f8 ? (bf16 ? rows_plan<true, true>(a.head_dim, two) : rows_plan<true, false>(a.head_dim, two))
-                          : (bf16 ? rows_plan<false, true>(a.head_dim, two) : rows_plan<false, false>(a.head_dim, two));
+    const RowsPlan p = f8 ? (bf16 ? rows_plan<true, true>(a.head_dim) : rows_plan<true, false>(a.head_dim))
+                          : (bf16 ? rows_plan<false, true>(a.head_dim) : rows_plan<false, false>(a.head_dim));
     const size_t smem = p.smem + size_t(a.n_seqs + 1) * sizeof(int);
     if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem + (kKvMaxSeqs + 1) * sizeof(int))) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_rows_kernel)");
@@ -1039,10 +1047,10 @@ extern "C" wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t
     // Sequences with up to kFewRows rows per key head are bound by reading their keys once and go
     // to the key-split kernel, the others to the tile kernel.  One launch where sequences bring that
     // few rows on average, right for any distribution; and where the call's rows are so few that
-    // tiles would leave most SMs idle, even if each key is read for several tiles of 16 rows.
-    // Tiles against split, us: heads of 128, 3000 keys, 1280 rows in all 80 / 44, 3200 rows 83 / 81,
-    // 6400 rows 80 / 134; 64 rows and 20000 keys 382 / 36; heads of 256, 1280 rows 88 / 67, 3200
-    // rows 89 / 128.
+    // tiles would leave most SMs idle, even if each key is read for several tiles of 8 rows.
+    // Tiles against split, us: heads of 128, 3000 keys, 1280 rows in all 80 / 37, 3200 rows 83 / 69,
+    // 6400 rows 79 / 119; 64 rows and 20000 keys 382 / 22; heads of 256, 1280 rows 88 / 51, 3200 rows
+    // 88 / 107.
     const bool bf16 = dt == WQ_BF16, f8 = cache->format == WQ_FMT_E4M3;
     const int64_t idle = int64_t(a.head_dim <= 128 ? 24 : 16) * device_info().sm_count;
     const bool tiles = M * a.group > kFewRows * batch->n_seqs && M * q_heads > idle;

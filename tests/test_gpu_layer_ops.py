@@ -241,6 +241,7 @@ APPEND = [
     ([0] * 30 + [100], [0] * 30 + [100], 2, 1, 256, 256, 256, "half"),
     ([9], [60], 2, 1, 132, 64, 132, "half"),
     ([2, 1], [40, 16], 3, 1, 36, 32, 18, "half"),
+    ([1] * 40 + [150, 8, 9], [7] * 40 + [160, 30, 31], 2, 1, 64, 64, 64, "half"),  # a chunk in a decode batch
 ]
 
 

@@ -21,7 +21,7 @@ HARNESS = r"""
 using namespace wq;
 extern "C" {
 void span(int lo, int hi, int len, int M, int cap, int *o) { KvSpan s = kv_span(lo, hi, len, M, cap); o[0] = s.q0; o[1] = s.n; o[2] = s.len; }
-long long item_start(int q0, int b, int sh) { return kv_item_start(q0, b, sh); }
+long long item_start(int q0, int b, int sh, int by) { return kv_item_start(q0, b, sh, by); }
 void page_span(int q0, int n, int len, long long k, int sh, int *o)
 { KvPageSpan r = kv_page_span(KvSpan{q0, n, len}, k, sh); o[0] = r.page; o[1] = r.off; o[2] = r.count; o[3] = r.token; }
 long long page_ok(int e, long long n) { return kv_page_ok(e, n); }
@@ -72,10 +72,12 @@ def test_spans_stay_inside_the_call(kv):
     assert _span(kv, 2, 5, 9, M, cap) == (2, 3, 9)
 
 
+@pytest.mark.parametrize("by_seq", [0, 1])
 @pytest.mark.parametrize("shift", [4, 5])
-def test_items_cover_every_new_token_once(kv, shift):
-    """For every way a sequence's new tokens lie on its pages: the items between two starts cover each
-    token with a place exactly once, in its page and slot, and the rest are idle."""
+def test_items_cover_every_new_token_once(kv, shift, by_seq):
+    """For every way a sequence's new tokens lie on its pages: the items between two starts (few
+    tokens: its first pages) cover each token with a place exactly once, in its page and slot, and
+    the rest are idle."""
     ps = 1 << shift
     for n in list(range(0, 3 * ps + 3)):
         for past in range(0, 2 * ps, 3 if n > 4 else 1):
@@ -84,9 +86,10 @@ def test_items_cover_every_new_token_once(kv, shift):
                 if ln < 0 or missing > n or (missing and past):
                     continue
                 for q0 in (0, 5, ps - 1, 3 * ps):
-                    first, end = kv.item_start(q0, 3, shift), kv.item_start(q0 + n, 4, shift)
+                    # sequences of few tokens walk their pages, the others' pages are items
+                    first, end = kv.item_start(q0, 3, shift, by_seq), kv.item_start(q0 + n, 4, shift, by_seq)
                     got = {}
-                    for k in range(end - first):
+                    for k in range(end - first if n > 8 else 4):
                         page, off, count, token = _page_span(kv, q0, n, ln, k, shift)
                         for i in range(count):
                             assert 0 <= off + i < ps
@@ -102,11 +105,11 @@ def test_an_item_before_the_sequence_is_idle(kv):
 
 def test_item_starts_never_overlap(kv):
     r = np.random.default_rng(0)
-    for shift in (4, 6, 8):
+    for shift, by_seq in itertools.product((4, 6, 8), (0, 1)):
         cu = np.concatenate([[0], np.cumsum(r.integers(0, 300, 50))])
-        starts = [kv.item_start(int(q), b, shift) for b, q in enumerate(cu)]
-        assert all(b - a >= 2 for a, b in zip(starts, starts[1:]))
-        assert starts[-1] <= (int(cu[-1]) >> shift) + 2 * 50
+        starts = [kv.item_start(int(q), b, shift, by_seq) for b, q in enumerate(cu)]
+        assert all(b - a >= 2 for a, b, n in zip(starts, starts[1:], np.diff(cu)) if n > 8)
+        assert starts == sorted(starts)
 
 
 def test_row_blocks_of_sequences_never_overlap(kv):
