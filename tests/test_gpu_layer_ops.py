@@ -65,7 +65,8 @@ def _norm_check(x, res, gamma, eps, dt, out):
 @pytest.mark.parametrize("out", ["int8", "fp8"])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("M,K", [(1, 8), (1, 4096), (3, 264), (5, 3200), (2, 4104), (2, 8640), (2, 11008), (1, 16384),
-                                 (2, 16392), (37, 128), (300, 1000)])
+                                 (2, 16392), (37, 128), (300, 1000),
+                                 (300, 1032), (300, 2056), (300, 4104)])
 def test_norm_bits(M, K, dtype, out):
     dt = DT[dtype]
     for residual in (True, False):
@@ -555,6 +556,39 @@ def test_calls_on_another_stream_and_in_a_graph():
     out = wq.kv_attention(q_d, cache, batch, workspace=ws, stream=side)
     side.synchronize()
     assert torch.equal(out, o_d)
+    del g
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_beside_decode_in_a_graph(D):
+    """Both attention kernels and a following matmul captured: every replay, back to back, gives the bits
+    of the plain calls (nothing starts before what it reads is written)."""
+    new, total = [300, 1, 20, 1], [420, 2000, 20, 64]
+    s = Setup(new, total, 16, 2, D, 32, "fp16", "fp8", seed=D).fill([120, 1999, 0, 63])
+    assert s.M * 16 > 24 * torch.cuda.get_device_properties(0).multi_processor_count
+    cache, batch = s.device()
+    ws = wq.make_workspace(wq.kv_attention_workspace_size(s.M, 16, cache, batch))
+    qc = wq.QuantConfig()
+    W, sc, _ = wq.quantize_pack(torch.randn(256, 16 * D, generator=torch.Generator().manual_seed(1)).cuda(), qc)
+    qkv, rope = _dev(s.qkv(), s.dt), torch.from_numpy(s.rope(D)).cuda()
+    mm = wq.make_workspace(wq.workspace_size(s.M, 256, 16 * D, qc))
+
+    def step():
+        q = wq.kv_append(qkv, cache, batch, 16, rope=rope)
+        o = wq.kv_attention(q, cache, batch, workspace=ws)
+        return q, o, wq.w4a16_gemm(o.view(s.M, -1), W, sc, None, 256, 16 * D, qc, workspace=mm)
+
+    want = step()  # (appending the same tokens again leaves the same cache: their pages' scales stand)
+    want = step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
     del g
 
 
