@@ -35,6 +35,10 @@ WQ_HD KvSpan kv_span(int cu_lo, int cu_hi, int seq_len, int M, int capacity)
     s.len = kv_clamp(seq_len, 0, capacity);
     return s;
 }
+// The same for an append, with the length as it is: cut to the capacity, the positions counted from it
+// would be those of earlier tokens.  Tokens from the limit (the capacity, or the rope table's
+// length) on have no place: kv_placed.
+WQ_HD KvSpan kv_append_span(int cu_lo, int cu_hi, int seq_len, int M) { return kv_span(cu_lo, cu_hi, seq_len, M, 0x7fffffff); }
 
 // An append's work: a sequence with up to kKvFewTokens tokens in the call is one item, and the
 // others' items are (sequence, page): sequence b with tokens q0 .. q1 - 1 owns those from
@@ -73,6 +77,14 @@ WQ_HD KvPageSpan kv_page_span(const KvSpan &s, int64_t k, int page_shift)
     r.count = last - first;
     r.token = s.q0 + (first - (s.len - s.n));
     return r;
+}
+
+// How many of a page's new tokens lie below the limit; not positive: none, and the page may be none of
+// the block table's.
+WQ_HD int kv_placed(const KvPageSpan &p, int page_shift, int limit)
+{
+    const int left = limit - ((p.page << page_shift) + p.off);
+    return p.count < left ? p.count : left;
 }
 
 // A physical page of the cache, or -1 where the block table's entry is out of range.

@@ -63,8 +63,7 @@ struct AppendArgs {
     int n_seqs, max_pages, M, q_heads;
     int rope_dim;
     int page_shift, pitch;
-    int capacity;       // tokens that the block table's row holds
-    int limit;          // positions below it have a place: min(capacity, rope_len)
+    int limit;          // positions below it have a place: those of the block table's row and of the rope table
     bool pairs;         // WQ_ROPE_PAIRS
     int items;          // (sequence, page) items of long runs
     int run_blocks;     // and the blocks that take them
@@ -316,16 +315,16 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, const T *src, c
 
 // Keys and values of one page of a sequence.
 template <typename T, bool F8, int WPT, int CH, Mode MODE>
-__device__ __forceinline__ void append_page(const AppendArgs &a, int b, int seq_len, const KvPageSpan &ps, int part, float *s_max)
+__device__ __forceinline__ void append_page(const AppendArgs &a, int b, const KvPageSpan &ps, int part, float *s_max)
 {
     constexpr int kTasks = kWarps / WPT;  // (head, keys or values) pairs of the block
     const int tid = threadIdx.x, warp = tid / 32;
     const int pos0 = (ps.page << a.page_shift) + ps.off;
-    const int count = min(ps.count, a.limit - pos0);  // positions beyond the rope table have no place
-    const int64_t page = kv_page_ok(__ldg(a.block_table + int64_t(b) * a.max_pages + ps.page), a.c.num_pages);
-    if (tid == 0 && (page < 0 || count < ps.count || seq_len > a.capacity))
-        atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
-    if (page < 0 || count <= 0) return;
+    const int count = kv_placed(ps, a.page_shift, a.limit);
+    const int64_t page =
+        count > 0 ? kv_page_ok(__ldg(a.block_table + int64_t(b) * a.max_pages + ps.page), a.c.num_pages) : -1;
+    if (tid == 0 && (page < 0 || count < ps.count)) atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
+    if (page < 0) return;
 
     const int task = warp / WPT, wi = warp % WPT;
     const int pair = part * kTasks + task;  // keys of head h, then its values
@@ -346,14 +345,13 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int b, int seq_
 template <typename T, bool F8, int CH, Mode MODE>
 __device__ __forceinline__ void append_few(const AppendArgs &a, int b, int part)
 {
-    const int len = __ldg(a.seq_len + b);
-    const KvSpan span = kv_span(__ldg(a.cu_q + b), __ldg(a.cu_q + b + 1), len, a.M, a.capacity);
+    const KvSpan span = kv_append_span(__ldg(a.cu_q + b), __ldg(a.cu_q + b + 1), __ldg(a.seq_len + b), a.M);
     if (span.n > kKvFewTokens) return;
 #pragma unroll 1
     for (int k = 0;; ++k) {
         const KvPageSpan ps = kv_page_span(span, k, a.page_shift);
         if (ps.count == 0) break;
-        append_page<T, F8, 1, CH, MODE>(a, b, len, ps, part, nullptr);
+        append_page<T, F8, 1, CH, MODE>(a, b, ps, part, nullptr);
     }
 }
 
@@ -383,9 +381,9 @@ __device__ __forceinline__ bool append_item(const AppendArgs &a, int item, int p
     if (!__syncthreads_or(any)) return false;
     const int b = s_seq[0];
     if (b >= 0) {
-        const KvSpan span = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
+        const KvSpan span = kv_append_span(s_seq[1], s_seq[2], s_seq[3], a.M);
         const KvPageSpan ps = kv_page_span(span, item - kv_item_start(span.q0, b, a.page_shift, RUNS), a.page_shift);
-        if (ps.count) append_page<T, F8, kWarps, CH, MODE>(a, b, s_seq[3], ps, part, s_max);
+        if (ps.count) append_page<T, F8, kWarps, CH, MODE>(a, b, ps, part, s_max);
     }
     return true;
 }
@@ -400,12 +398,11 @@ __device__ __forceinline__ void turn_queries(const AppendArgs &a, int64_t block)
     if (tid < kWarps) s_pos[tid] = -2;
     __syncthreads();
     for (int b = tid; b < a.n_seqs; b += kThreads) {
-        const int len = a.seq_len[b];
-        const KvSpan s = kv_span(a.cu_q[b], a.cu_q[b + 1], len, a.M, a.capacity);
+        const KvSpan s = kv_append_span(a.cu_q[b], a.cu_q[b + 1], a.seq_len[b], a.M);
         for (int64_t m = max(int64_t(s.q0), m0); m < min(int64_t(s.q0) + s.n, m0 + a.q_tokens); ++m) {
             const int p = s.len - s.n + int(m - s.q0);
             s_pos[m - m0] = p < 0 || p >= a.limit ? -1 : p;
-            if (p >= a.limit || len > a.capacity) atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
+            if (p >= a.limit) atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
         }
     }
     __syncthreads();
@@ -560,8 +557,8 @@ extern "C" wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t 
     a.rope_dim = rope_dim;
     while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
     a.pitch = kv_pitch(cache->head_dim);
-    a.capacity = int(batch->max_pages * cache->page_size);
-    a.limit = rope ? int(std::min<int64_t>(a.capacity, rope_len)) : a.capacity;
+    const int64_t capacity = batch->max_pages * cache->page_size;
+    a.limit = int(rope ? std::min(capacity, rope_len) : capacity);
     a.pairs = rope_style == WQ_ROPE_PAIRS;
     // kHalf: partners and cos / sin at rope_dim / 2, a table row rope_dim values long; see Mode
     const Mode mode = !rope_dim                           ? kNone

@@ -1,0 +1,57 @@
+"""Calls of the layer operators at the edges of what their documentation allows: lengths beyond
+the block table, tiny, zero and huge scales and scores, in each attention kernel."""
+import numpy as np
+import pytest
+import torch
+
+import gemv_wq_quantize_b200 as wq
+import layer_reference as ref
+from test_gpu_layer_ops import MARK, U, Setup, _append, _attend, _attend_check, _bound, _lib, _many, _np  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- append: lengths beyond the block table
+def _rope(positions, r):
+    ang = np.arange(positions)[:, None] * 10000.0 ** (-np.arange(0, r, 2) / r)
+    return np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+
+
+BEYOND = [
+    # new, lengths (table: 4 pages of 16), rope
+    ([1, 1], [65, 30], True),
+    ([4, 1], [66, 30], False),                        # two of four fit
+    ([8, 2], [1000, 30], True),
+    ([1, 1], [2 ** 31 - 1, 30], False),
+    ([40, 1], [80, 30], True),                        # a long run, part of which fits
+    ([30, 40], [90, 50], False),                      # none of it does
+    ([12] + [1] * 20, [2 ** 31 - 1] + [30] * 20, True),
+]
+
+
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+@pytest.mark.parametrize("case", BEYOND, ids=lambda c: "q%s_len%s" % (c[0][0], c[1][0]))
+def test_append_beyond_the_block_table(case, out):
+    """Tokens at or behind the table's capacity are left out: no slot, scale or code of an earlier token
+    changes, their queries are zeros, the tokens that fit are stored, and the error word says so."""
+    new, total, turned = case
+    fit = [min(t, 64) for t in total]
+    s = Setup(new, fit, 4, 2, 32, 16, "fp16", out, seed=sum(new))
+    s.fill([max(f - n, 0) if t <= 64 else min(max(t - n, 0), 64) for n, t, f in zip(new, total, fit)])
+    s.table, s.total = np.ascontiguousarray(s.table[:, :4]), total
+    s.table[s.table == 1 << 30] = 0  # (tables are padded with a valid page, another sequence's perhaps)
+    rope = _rope(200, 32) if turned else None
+    cache, batch = s.device()
+    qkv = s.qkv() * 4  # larger than what the pages hold: a stray token would raise their scales
+    qkv = ref.to_t(qkv, s.dt)
+    got = _append(s, qkv, rope, "half", cache, batch)
+    torch.cuda.synchronize()
+    assert wq.device_error() == 3
+    want = np.zeros((s.M, 4, 32))
+    for b, (n, t) in enumerate(zip(new, total)):
+        first, placed = int(s.cu[b]), max(0, min(n, 64 - (t - n)))
+        ref.append_bits(qkv, s.host, [first, first + placed], [t - n + placed], s.table[b: b + 1], 4, 2, rope, "half", s.dt, want)
+    assert np.array_equal(_np(got), want)
+    assert np.array_equal(_np(cache.k_scale), s.host.ks.astype(np.float64), equal_nan=True)
+    assert np.array_equal(_np(cache.v_scale), s.host.vs.astype(np.float64), equal_nan=True)
+    assert np.array_equal(cache.k.cpu().numpy(), s.host.k) and np.array_equal(cache.v.cpu().numpy(), s.host.v)
