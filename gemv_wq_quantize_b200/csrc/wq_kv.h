@@ -16,6 +16,7 @@ namespace wq {
 constexpr int kKvMaxSeqs = 4096;       // sequences of one call (their unit counts are summed in shared memory)
 constexpr int kKvMaxHeadDim = 256;
 constexpr int kKvMinPage = 16, kKvMaxPage = 256;
+constexpr int kKvMaxTokens = 0x7fffffff - 1023;  // of a block table's row: steps of keys are counted past the last one
 
 WQ_HD int kv_pitch(int head_dim) { return (head_dim + 15) & ~15; }
 

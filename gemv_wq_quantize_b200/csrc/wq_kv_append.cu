@@ -512,8 +512,8 @@ wq_status check_kv(const wq_kv_cache *c, const wq_kv_batch *b, wq_dtype dt, int6
     if (M > 0x7fffffff / int64_t(q_heads)) return fail(WQ_ERR_INVALID_ARG, "M * q_heads exceeds int32");
     if (b->n_seqs < 1) return fail(WQ_ERR_INVALID_ARG, "n_seqs must be positive");
     if (b->n_seqs > kKvMaxSeqs) return fail(WQ_ERR_UNSUPPORTED, "n_seqs must be at most %d", kKvMaxSeqs);
-    if (b->max_pages < 1 || b->max_pages > 0x7fffffff / c->page_size)
-        return fail(WQ_ERR_INVALID_ARG, "max_pages must be positive, and max_pages * page_size below 2^31");
+    if (b->max_pages < 1 || b->max_pages > kKvMaxTokens / c->page_size)
+        return fail(WQ_ERR_INVALID_ARG, "max_pages must be positive, and max_pages * page_size at most 2^31 - 1024");
     if (!c->k || !c->v || !c->k_scale || !c->v_scale || !b->cu_q || !b->seq_len || !b->block_table)
         return fail(WQ_ERR_INVALID_ARG, "the pointers of cache and batch must be non-null");
     if (!aligned16(c->k) || !aligned16(c->v)) return fail(WQ_ERR_ALIGNMENT, "k and v must be 16-byte aligned");

@@ -286,7 +286,7 @@ typedef struct {
  *   p = seq_len[b] - (cu_q[b+1] - cu_q[b]) + i.
  * Token p lives in page block_table[b, p / page_size], slot p % page_size.
  *   cu_q [n_seqs + 1], seq_len [n_seqs], block_table [n_seqs, max_pages] int32; entries beyond a
- *   sequence's last page are not read.  n_seqs 1 to 4096; max_pages * page_size < 2^31.
+ *   sequence's last page are not read.  n_seqs 1 to 4096; max_pages * page_size at most 2^31 - 1024.
  * A row with a negative position (an idle slot of a fixed-size batch: seq_len 0) has no place:
  * kv_append stores nothing for it and kv_attention gives zeros.  Rows from cu_q[n_seqs] on are
  * left as they were.  Sequences may share pages that they only read; a page that a call writes

@@ -52,3 +52,30 @@ def test_append_places_tokens_below_the_limit_only(kv, limit):
                 got[token + i] = page * 16 + off + i
         total = max(total, 0)
         assert got == {3 + i: total - n + i for i in range(n) if 0 <= total - n + i < limit}, (n, total)
+
+
+# ---------------------------------------------------------------- refusals
+@pytest.fixture(scope="module")
+def lib():
+    from gemv_wq_quantize_b200 import build
+    build.build(quiet=True)
+    return wq.load_library()
+
+
+def _calls(lib, cache, batch):
+    """The status of an append and of an attention call, nothing of which is launched if they refuse."""
+    fake = ctypes.c_void_p(0x10000)
+    return (lib.kv_append(fake, wq.WQ_F16, 4, 4, None, 0, 0, 0, fake, cache, batch, None),
+            lib.kv_attention(fake, wq.WQ_F16, 4, 4, cache, batch, 1.0, fake, None, 0, None))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_a_table_row_ends_well_below_2_to_the_31(lib, page):
+    """The kernels look up to a step of keys past the last one in 32 bits, so the last 1023 positions are
+    refused."""
+    cache = wq._KVCacheC(0x10000, 0x10000, 0x10000, 0x10000, 8, page, 2, 128, wq.FMT_INT)
+    for pages in ((2 ** 31 - 1023) // page + 1, (2 ** 31 - 1) // page):
+        batch = wq._KVBatchC(0x10000, 0x10000, 0x10000, 2, pages)
+        assert _calls(lib, cache, batch) == (wq.WQ_ERR_INVALID_ARG,) * 2
+    batch = wq._KVBatchC(0x10000, 0x10000, 0x10000, 2, (2 ** 31 - 1024) // page)
+    assert lib.kv_attention_workspace_size(4, 4, cache, batch) > 0
