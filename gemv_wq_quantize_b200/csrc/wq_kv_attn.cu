@@ -834,11 +834,14 @@ __device__ __forceinline__ void attend_rows(const CUtensorMap &km, const CUtenso
         tma_prefetch_desc(&km);
         tma_prefetch_desc(&vm);
     }
+    if (!a.behind_tiles) grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
+    // Behind the wait: a kernel ahead that let its dependents start before it had its own Tensor Memory
+    // would otherwise wait for columns that this block holds while it waits for that kernel.  (The tile
+    // kernel of the same call holds its own by then.)
     if (warp == kMmaWarp) {
         tc::tmem_alloc(&sm.tmem, S::kTmem);
         tc::tmem_relinquish();
     }
-    if (!a.behind_tiles) grid_dep_wait();  // queries, cache and batch arrays may come from the kernel before
 
     // units of every sequence, summed up: each thread takes a run of sequences
     const bool split = a.partials != nullptr;

@@ -63,6 +63,10 @@
  *     pointer not 16-byte aligned), WQ_ERR_UNSUPPORTED (a valid request this build does not
  *     implement, e.g. a group size that is not a multiple of 128).  A failed launch returns
  *     WQ_ERR_CUDA.  wq_last_error() gives a one-line reason for the calling thread.
+ *   - Kernels start by programmatic dependent launch and wait on the device for what is ahead of them.
+ *     The matmuls above 16 tokens take their Tensor Memory before that wait, so a kernel of another
+ *     library ahead in the stream may let its dependents start early (griddepcontrol.
+ *     launch_dependents) only once it holds the Tensor Memory that it needs.
  *   - Nothing traps on the device.
  */
 #ifndef WQ_H

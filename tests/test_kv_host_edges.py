@@ -79,3 +79,14 @@ def test_a_table_row_ends_well_below_2_to_the_31(lib, page):
         assert _calls(lib, cache, batch) == (wq.WQ_ERR_INVALID_ARG,) * 2
     batch = wq._KVBatchC(0x10000, 0x10000, 0x10000, 2, (2 ** 31 - 1024) // page)
     assert lib.kv_attention_workspace_size(4, 4, cache, batch) > 0
+
+
+# ---------------------------------------------------------------- order in the kernels
+@pytest.mark.parametrize("source", ["wq_kv_attn.cu", "wq_kv_tiles.cu"])
+def test_tensor_memory_is_taken_between_the_wait_and_the_next_launch(source):
+    """A block that held Tensor Memory while it waited for a kernel that still wanted some would lock both
+    up, and so would a next kernel's block that was let in before this one had its own."""
+    with open(os.path.join(ROOT, "gemv_wq_quantize_b200", "csrc", source)) as f:
+        text = "\n".join(line.split("//")[0] for line in f)
+    wait, take, launch = (text.index(w) for w in ("grid_dep_wait();", "tmem_alloc(", "grid_dep_launch();"))
+    assert wait < take < launch
