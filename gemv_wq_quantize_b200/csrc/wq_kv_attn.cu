@@ -594,7 +594,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs &a, Smem<NB, NR> &sm, co
                 f_now[r] = fm * fv;
             }
         }
-        const float v = gone || st.vref == 0.f ? 0.f : sm.vs[slot][tid / 16] * (inverse_pow2(st.vref) * kPUp<F8>);
+        // (the scale over vref first, which is below 1: 2^26 / vref may be beyond binary32)
+        const float v = gone || st.vref == 0.f ? 0.f : sm.vs[slot][tid / 16] * inverse_pow2(st.vref) * kPUp<F8>;
         float w[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -652,11 +653,11 @@ __device__ __forceinline__ void finish(const KvAttnArgs &a, Smem<NB, NR> &sm, co
     for (int r = 0; r < NR; ++r) {
         if (r >= t.rows) break;
         const float l = sm.sum[0][r] + sm.sum[1][r] + sm.sum[2][r] + sm.sum[3][r];
-        const float scale = slot ? st.vref : st.vref * inverse_of(l);
+        const float inv = slot ? 1.f : inverse_of(l);  // (before vref: vref / l may be below the normal numbers)
 #pragma unroll
         for (int c = 0; c < NB; ++c) {
             const int d = 128 * c + tid;
-            const float x = st.vref > 0.f ? st.o[c][r] * scale : (l == l ? 0.f : l);
+            const float x = st.vref > 0.f ? st.o[c][r] * inv * st.vref : (l == l ? 0.f : l);
             if (slot) slot[r * S::kRowFloats + d] = x;
             else if (d < a.head_dim) static_cast<T *>(a.out)[sm.row_at[r] + d] = act_t<T>(x);
         }

@@ -55,3 +55,30 @@ def test_append_beyond_the_block_table(case, out):
     assert np.array_equal(_np(cache.k_scale), s.host.ks.astype(np.float64), equal_nan=True)
     assert np.array_equal(_np(cache.v_scale), s.host.vs.astype(np.float64), equal_nan=True)
     assert np.array_equal(cache.k.cpu().numpy(), s.host.k) and np.array_equal(cache.v.cpu().numpy(), s.host.v)
+
+
+# ---------------------------------------------------------------- attention: tiny and zero value scales
+def _scaled(s, workspaces, vs):
+    """The setup's value scales times a power of two, and its attention within the usual bound plus half a
+    step of the smallest bfloat16 values."""
+    used = np.isfinite(s.host.vs)
+    s.host.vs[used] = (s.host.vs[used].astype(np.float64) * vs).astype(np.float32)
+    cache, batch = s.device()
+    q = s.q()
+    want, mass, score, top, own = ref.attention_64(q, s.host, s.cu, s.total, s.table, float(np.float32(s.D ** -0.5)), s.num_pages)
+    for ws in workspaces:
+        g = _np(_attend(s, q, cache, batch, workspace=ws))
+        lim = _bound(want, mass, score, top, max(s.total), s.dtype) + 1.01 * 2.0 ** -134
+        assert np.isfinite(g[own]).all() and (np.abs(g - want)[own] <= lim[own]).all(), \
+            np.max(np.abs(g - want)[own] / lim[own])
+
+
+VALUE_SCALES = [0.0, 2.0 ** -97, 2.0 ** -108, 2.0 ** -118, 2.0 ** -126, 2.0 ** 100, 2.0 ** 117]
+
+
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("vs", VALUE_SCALES)
+def test_attention_value_scales_of_any_size(vs, D, out):
+    """Few rows.  The scales are 2^-7 .. 2^-4 (INT8) times vs; all are valid in a cache."""
+    _scaled(Setup([1, 3], [700, 90], 4, 2, D, 32, "bf16", out, seed=7).fill([700, 90]), (True, None), vs)
