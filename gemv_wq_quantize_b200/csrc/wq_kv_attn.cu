@@ -568,7 +568,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs &a, Smem<NB, NR> &sm, co
         const float vmax = sm.v_max[slot];
         bool rose = vmax >= st.vref && vmax > 0.f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) rose |= !(s[r] <= st.m[r] + kSlack);  // (NaN too)
+        for (int r = 0; r < NR; ++r) rose |= !(s[r] <= __fadd_rd(st.m[r], kSlack));  // (NaN too; rounded up it may be m + 4)
         if (soft_any(rose)) {
             int mine = 0;
 #pragma unroll

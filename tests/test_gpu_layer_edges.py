@@ -82,3 +82,32 @@ VALUE_SCALES = [0.0, 2.0 ** -97, 2.0 ** -108, 2.0 ** -118, 2.0 ** -126, 2.0 ** 1
 def test_attention_value_scales_of_any_size(vs, D, out):
     """Few rows.  The scales are 2^-7 .. 2^-4 (INT8) times vs; all are valid in a cache."""
     _scaled(Setup([1, 3], [700, 90], 4, 2, D, 32, "bf16", out, seed=7).fill([700, 90]), (True, None), vs)
+
+
+# ---------------------------------------------------------------- attention: huge scores
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+def test_attention_scores_a_step_apart(out):
+    """Scores of 2^25 and more in base 2, where one step of binary32 is 4: a key one or two steps over the
+    reference weighs 16 or 256 times as much, in a later step of 128 keys too."""
+    s = Setup([1], [256], 1, 1, 64, 32, "bf16", out, seed=3).fill([256])
+    log2e = np.float32(1.4426950408889634)
+    sm = np.float32(2 ** 19 / 1.4426950408889634)
+    assert np.float32(sm * log2e) == 2 ** 19  # as the kernel forms it
+    at = np.arange(256)
+    pages, slots = s.table[0, at // 32], at % 32
+    c = np.zeros((256, 64))
+    c[:, 0] = 64
+    step = np.zeros(256)
+    step[5], step[200], step[210] = 1, 2, 1
+    c[:, 1] = step
+    s.host.k[pages, 0, slots, :64] = ref.codes_of(c, 1, out)
+    s.host.ks[:] = np.where(np.isfinite(s.host.ks), 1.0, s.host.ks)
+    q = np.zeros((1, 1, 64))
+    q[0, 0, :2] = 1, 2.0 ** -17  # the score: 2^19 (64 + step 2^-17) = 2^25 + 4 step
+    cache, batch = s.device()
+    got = _np(_attend(s, ref.to_t(q, s.dt), cache, batch, sm_scale=float(sm)))[0, 0]
+    w = 2.0 ** (4 * step)
+    v = ref.values_of(s.host.v[pages, 0, slots, :64], out) * s.host.vs[pages, 0].astype(np.float64)[:, None]
+    want, mass = w @ v / w.sum(), w @ np.abs(v) / w.sum()
+    # scores and weights are exact powers of two: value scale and its parts (2^-16), the sums, the type
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) * 1.01 + (2.0 ** -16 + 2.0 ** -18) * mass).all()
