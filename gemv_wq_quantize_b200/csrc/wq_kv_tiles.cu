@@ -84,6 +84,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 constexpr int kRing = 4;             // scale sets: a set is rewritten once both tiles are two steps on
 constexpr uint32_t kTmemCols = 512, kScol = 0, kOcol = 256;  // two 128-column tiles of each
 
+// Value scales that may be part of the weights' exponent (weights_once): the least is 2^-81 of the
+// reference above the largest, so that a weight vanishes only under 2^-55 and a group's sum over its
+// scale stays within binary32.
+constexpr float kLeastPlain = 0x1p-48f, kMostPlain = 0x1p32f;
+
 // Weights are raised by 2^kRaise: exact to half a step down to 2^-(14 + kRaise) in binary16.  A
 // maximum that rises a little is not followed while all weights fit: 2^kRaise times the rise.
 constexpr float kRaise = 11.f;
@@ -98,7 +103,7 @@ struct Scales {
     float log_v[kRing][kMaxGroups], inv_v[kRing][kMaxGroups];
     float v_max[kRing];
     uint32_t dead[kRing];          // groups whose block-table entry is no page
-    int plain[kRing];              // no dead groups, all value scales positive normal numbers
+    int plain[kRing];              // no dead groups, all value scales in kLeastPlain .. kMostPlain
 };
 
 // DT: the head's size rounded up to 64, 128 or 256.  Up to 128: two tiles of 128 rows, steps of 128
@@ -216,7 +221,7 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, co
         const int set = j % kRing, g = lane - kGroups;
         const bool bad = grouped && used && z < 0;
         const uint32_t dead = __ballot_sync(0xffffffffu, bad) >> kGroups;
-        const bool normal = vs >= 0x1p-126f && vs <= 0x1p126f;
+        const bool normal = vs >= kLeastPlain && vs <= kMostPlain;
         // (groups behind the last key: masked by their keys, any scale will do)
         const bool plain = __all_sync(0xffffffffu, !grouped || !used || normal) && !dead;
         const float top = __uint_as_float(warp_umax(__float_as_uint(fabsf(vs))));
@@ -516,7 +521,7 @@ __device__ __forceinline__ bool new_references(uint32_t scol, uint32_t ocol, con
     return true;
 }
 
-// The weights of a step with groups that are no pages or value scales that have no logarithm.
+// The weights of a step with groups that are no pages or value scales that weights_once does not take.
 template <int GROUPS>
 __device__ __forceinline__ void weights_any(uint32_t scol, const Scales &sc, int set, float unscale, int left, uint32_t dead,
                                             float m, float vref, float &l)
@@ -669,7 +674,8 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
     tc::fence_after_sync();
     // ---- the finished rows: through the warp's part of the query rows' memory (its products are
     // done), so that rows leave as whole lines
-    const float inv = l > 0.f ? vref / l : (l == l ? 0.f : l);
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);  // (vref / l may be below the normal numbers)
+    const uint32_t keep = l == 0.f ? 0u : ~0u;
     uint8_t *back = qsm + tile * Layout<DT>::kQ + 32 * (warp % 4) * (2 * DT);
     if (steps == 0) named_bar_sync(1 + tile, kTile);  // (no product said that all query rows are written)
 #pragma unroll 1
@@ -684,9 +690,8 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = l == 0.f ? 0.f : __uint_as_float(o[8 * k + 2 * e]) * inv;
-                const float y = l == 0.f ? 0.f : __uint_as_float(o[8 * k + 2 * e + 1]) * inv;
-                h[e] = act_t2<T>(x, y);
+                const float x = __uint_as_float(o[8 * k + 2 * e]) * inv * vref, y = __uint_as_float(o[8 * k + 2 * e + 1]) * inv * vref;
+                h[e] = act_t2<T>(x, y) & keep;
             }
             sts128(back + lane * (2 * DT) + (((4 * c + k) ^ (lane & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
         }

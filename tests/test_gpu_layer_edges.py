@@ -84,6 +84,40 @@ def test_attention_value_scales_of_any_size(vs, D, out):
     _scaled(Setup([1, 3], [700, 90], 4, 2, D, 32, "bf16", out, seed=7).fill([700, 90]), (True, None), vs)
 
 
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("vs", VALUE_SCALES)
+def test_attention_many_rows_value_scales_of_any_size(vs, D, out):
+    new = [130, 40]
+    _scaled(Setup(new, [300, 40], *_many(new, 2, 1), D, 32, "bf16", out, seed=8).fill([300, 40]), (True,), vs)
+
+
+@pytest.mark.parametrize("dtype,out", [("fp16", "int8"), ("fp16", "fp8"), ("bf16", "int8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("sm,size", [(3.0, 1.0), (0.0, 1.0), (-0.2, 1.0), (0.1, 1e-30), (1e-5, 1e4)])
+def test_attention_many_rows_scores_of_any_size(sm, size, D, dtype, out):
+    """One weight that takes all, a zero scale (a plain mean), a negative one, tiny and large queries."""
+    new = [140, 60]
+    s = Setup(new, [200, 90], *_many(new, 2, 1), D, 32, dtype, out, seed=7).fill([200, 90])
+    q = ref.to_t(s.q() * size, s.dt)
+    cache, batch = s.device()
+    _attend_check(s, q, _attend(s, q, cache, batch, sm_scale=sm), sm)
+
+
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+@pytest.mark.parametrize("D,many", [(64, False), (64, True), (128, True), (256, False), (256, True)])
+def test_attention_value_scales_very_far_apart(D, many, out):
+    """Pages whose values are next to nothing beside the others' still count in the sum of the weights."""
+    new = [130] if many else [3]
+    s = Setup(new, [400], *(_many(new, 2, 1) if many else (4, 2)), D, 32, "bf16", out, seed=10).fill([400])
+    r = np.random.default_rng(4)
+    used = np.isfinite(s.host.vs)
+    s.host.vs[used] = (2.0 ** r.uniform(-140, 3, used.sum())).astype(np.float32)
+    q = s.q()
+    cache, batch = s.device()
+    _attend_check(s, q, _attend(s, q, cache, batch))
+
+
 # ---------------------------------------------------------------- attention: huge scores
 @pytest.mark.parametrize("out", ["int8", "fp8"])
 def test_attention_scores_a_step_apart(out):
