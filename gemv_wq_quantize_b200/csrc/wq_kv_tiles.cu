@@ -89,6 +89,10 @@ constexpr uint32_t kTmemCols = 512, kScol = 0, kOcol = 256;  // two 128-column t
 // scale stays within binary32.
 constexpr float kLeastPlain = 0x1p-48f, kMostPlain = 0x1p32f;
 
+// Up to here weights_once takes a row's maximum: it and the shifts are one binary32 number there, off by
+// half a step of it (2^-4; from 2^26 on weights would not fit binary16).
+constexpr float kWide = 0x1p20f;
+
 // Weights are raised by 2^kRaise: exact to half a step down to 2^-(14 + kRaise) in binary16.  A
 // maximum that rises a little is not followed while all weights fit: 2^kRaise times the rise.
 constexpr float kRaise = 11.f;
@@ -521,12 +525,13 @@ __device__ __forceinline__ bool new_references(uint32_t scol, uint32_t ocol, con
     return true;
 }
 
-// The weights of a step with groups that are no pages or value scales that weights_once does not take.
+// The weights of a step with groups that are no pages, or with value scales or a maximum that weights_once
+// does not take, after new_references: no score is over the maximum.
 template <int GROUPS>
 __device__ __forceinline__ void weights_any(uint32_t scol, const Scales &sc, int set, float unscale, int left, uint32_t dead,
                                             float m, float vref, float &l)
 {
-    const float base = m == -INFINITY ? 0.f : m - kRaise, inv = vref > 0.f ? 1.f / vref : 0.f;
+    const float top = m == -INFINITY ? 0.f : m, inv = vref > 0.f ? 1.f / vref : 0.f;
 #pragma unroll 1
     for (int g = 0; g < GROUPS; ++g) {
         uint32_t s[16], p[8];
@@ -539,7 +544,8 @@ __device__ __forceinline__ void weights_any(uint32_t scol, const Scales &sc, int
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                w[e] = exp2_approx(fmaf(__uint_as_float(s[x + e]), k, -base));
+                // (the product as new_references rounds it: never over the maximum)
+                w[e] = exp2_approx(__fmul_rn(__uint_as_float(s[x + e]), k) - top + kRaise);
                 if (16 * g + x + e >= left || gone) w[e] = 0.f;
             }
             l += w[0] + w[1];
@@ -643,14 +649,16 @@ __device__ void softmax_role(const KvAttnArgs &a, const Item &t, uint8_t *qsm, c
         // vs / vref.
         const uint32_t dead = sc.dead[set];
         const bool all_seen = least >= kKeys, plain = sc.plain[set];
-        bool refer = j == 0 || !plain || !__all_sync(0xffffffffu, sc.v_max[set] < vref && (m > -INFINITY || left <= 0));
+        bool refer = j == 0 || !plain || !__all_sync(0xffffffffu, sc.v_max[set] < vref && (fabsf(m) <= kWide || left <= 0));
 #pragma unroll 1
         for (;;) {
-            if (refer && !new_references<DT>(scol, ocol, sc, set, unscale, left, all_seen && !dead, dead, j, tile, bar, abort, m, vref, l))
-                return;
-            if (!plain) {
-                weights_any<kGroups>(scol, sc, set, unscale, left, dead, m, vref, l);
-                break;
+            if (refer) {
+                if (!new_references<DT>(scol, ocol, sc, set, unscale, left, all_seen && !dead, dead, j, tile, bar, abort, m, vref, l))
+                    return;
+                if (!plain || __any_sync(0xffffffffu, fabsf(m) > kWide && left > 0)) {
+                    weights_any<kGroups>(scol, sc, set, unscale, left, dead, m, vref, l);
+                    break;
+                }
             }
             const float shift = kRaise - (m == -INFINITY ? 0.f : m) - float(int(__float_as_uint(vref) >> 23) - 127);
             float lsum = 0.f;

@@ -145,3 +145,32 @@ def test_attention_scores_a_step_apart(out):
     want, mass = w @ v / w.sum(), w @ np.abs(v) / w.sum()
     # scores and weights are exact powers of two: value scale and its parts (2^-16), the sums, the type
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) * 1.01 + (2.0 ** -16 + 2.0 ** -18) * mass).all()
+
+
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D,many", [(64, False), (128, True), (256, False), (256, True)])
+def test_attention_huge_scores(D, many, dtype, out):
+    """Scores of 2^20 to 2^90 in base 2, with one key far above the others, which comes late: the result
+    is that key's value (every other weight is 0)."""
+    new = [140] if many else [3]
+    heads = _many(new, 2, 1) if many else (2, 1)
+    s = Setup(new, [700], *heads, D, 16, dtype, out, seed=9).fill([700])
+    r = np.random.default_rng(1)
+    at = np.arange(700)
+    pages, slots = s.table[0, at // 16], at % 16
+    code = np.minimum(np.arange(700) // 8, 90).astype(np.float64)  # the maximum rises step by step
+    code[525] = 120
+    s.host.k[pages, :, slots, 0] = ref.codes_of(code, 1, out)[:, None]
+    s.host.ks[:] = np.where(np.isfinite(s.host.ks), 2.0 ** 40 if dtype == "fp16" else 1.0, s.host.ks)
+    q = np.zeros((s.M, s.q_heads, D))
+    q[..., 0] = 2.0 ** (r.uniform(-12, 12, q.shape[:2]) if dtype == "fp16" else r.uniform(15, 80, q.shape[:2]))
+    q = ref.to_t(q, s.dt)
+    cache, batch = s.device()
+    got = _np(_attend(s, q, cache, batch, sm_scale=0.3))
+    p, i = s.table[0, 525 // 16], 525 % 16
+    v = ref.values_of(s.host.v[p, :, i, :D], out) * s.host.vs[p].astype(np.float64)[:, None]
+    want = np.repeat(v, s.q_heads // heads[1], 0)[None]
+    # the weight's own 16 (or 8-bit parts': 16) bits, the type's rounding, the exponential and 1 / sum
+    lim = (U[dtype] + 2.0 ** -11 + 2.0 ** -18) * np.abs(want) * 1.01
+    assert np.isfinite(got).all() and (np.abs(got - want) <= lim).all()
