@@ -602,8 +602,12 @@ def _append_call(raw, qkv, cache, batch, q_heads, rope, rope_len, rope_dim, rope
 
 
 def kv_attention_workspace_size(M: int, q_heads: int, cache: KVCache, batch: KVBatch) -> int:
+    """Bytes of workspace for :func:`kv_attention` (an error where that call would be refused)."""
     with torch.cuda.device(cache.device):
-        return int(load_library().kv_attention_workspace_size(M, q_heads, cache._c, batch._c))
+        n = int(load_library().kv_attention_workspace_size(M, q_heads, cache._c, batch._c))
+    if n == 0:
+        _check(WQ_ERR_INVALID_ARG, "kv_attention_workspace_size")
+    return n
 
 
 def kv_attention(q, cache: KVCache, batch: KVBatch, sm_scale: float | None = None, out=None, workspace=None,

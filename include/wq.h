@@ -342,7 +342,8 @@ wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t q_heads, co
  *   q, out [M, q_heads * head_dim] of type dt (WQ_F16 or WQ_BF16); sm_scale finite.
  *   workspace: as for w4a16_gemm (kv_attention_workspace_size bytes, zero-filled once, shared by
  *   calls that do not overlap); lets few rows over long contexts spread over the whole GPU.
- *   NULL or too small: every key range is walked by one block.
+ *   NULL or too small: every key range is walked by one block.  (The size is 0 for arguments that the
+ *   call would refuse.)
  * Results do not depend on timing: the same call on the same device gives the same bits. */
 wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t q_heads, const wq_kv_cache *cache,
                        const wq_kv_batch *batch, float sm_scale, void *out, void *workspace, size_t ws_bytes,

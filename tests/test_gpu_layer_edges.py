@@ -174,3 +174,14 @@ def test_attention_huge_scores(D, many, dtype, out):
     # the weight's own 16 (or 8-bit parts': 16) bits, the type's rounding, the exponential and 1 / sum
     lim = (U[dtype] + 2.0 ** -11 + 2.0 ** -18) * np.abs(want) * 1.01
     assert np.isfinite(got).all() and (np.abs(got - want) <= lim).all()
+
+
+# ---------------------------------------------------------------- the binding
+def test_workspace_size_of_an_invalid_call_is_an_error():
+    cache = wq.make_kv_cache(4, 16, 2, 64)
+    i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    batch = wq.KVBatch(i, i[:2], torch.zeros(2, 4, dtype=torch.int32, device="cuda"))
+    assert wq.kv_attention_workspace_size(4, 4, cache, batch) > 0
+    for M, heads in ((0, 4), (4, 3), (4, 0), (2 ** 30, 4)):
+        with pytest.raises(wq.WqError):
+            wq.kv_attention_workspace_size(M, heads, cache, batch)
