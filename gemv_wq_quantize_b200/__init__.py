@@ -540,6 +540,8 @@ class KVCache:
 def make_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, format: int = FMT_INT,
                   device=None) -> KVCache:
     """A new cache of INT8 (FMT_INT) or e4m3 (FMT_E4M3) codes."""
+    if format not in (FMT_INT, FMT_E4M3):
+        raise ValueError("format must be FMT_INT or FMT_E4M3")
     device = device or "cuda"
     shape = (num_pages, kv_heads, page_size, -(-head_dim // 16) * 16)
     dt = torch.int8 if format == FMT_INT else torch.uint8

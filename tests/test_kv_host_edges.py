@@ -81,6 +81,12 @@ def test_a_table_row_ends_well_below_2_to_the_31(lib, page):
     assert lib.kv_attention_workspace_size(4, 4, cache, batch) > 0
 
 
+@pytest.mark.parametrize("format", [wq.FMT_E2M1, 3, -1])
+def test_a_cache_holds_int8_or_e4m3(format):
+    with pytest.raises(ValueError, match="format"):
+        wq.make_kv_cache(4, 16, 2, 128, format=format)
+
+
 # ---------------------------------------------------------------- order in the kernels
 @pytest.mark.parametrize("source", ["wq_kv_attn.cu", "wq_kv_tiles.cu"])
 def test_tensor_memory_is_taken_between_the_wait_and_the_next_launch(source):
