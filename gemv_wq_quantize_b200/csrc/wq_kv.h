@@ -106,10 +106,31 @@ WQ_HD int64_t kv_scale_index(int64_t page, int head, int heads) { return page * 
 WQ_HD int64_t kv_tiles(int n, int group, int rows) { return (int64_t(n) * group + rows - 1) / rows; }
 WQ_HD int kv_units(int len, int shift) { return len > 0 ? int((int64_t(len) + (int64_t(1) << shift) - 1) >> shift) : 1; }
 
+// Which sequences go to the tile kernel: those with more rows per key head than this.  None where all
+// rows together are at most `idle` (too few for its blocks), or where sequences bring at most
+// kKvFewRows on average and the rows beyond one token a sequence are at most twice `idle`: a decode or
+// draft batch.  If those are more, some sequence may be a long one among short ones (the host knows
+// their number only): then what has more than `idle` rows by itself.
+constexpr int kKvFewRows = 16;
+WQ_HD int kv_few_rows(int64_t M, int64_t n_seqs, int q_heads, int kv_heads, int64_t idle)
+{
+    const int64_t rows = M * (q_heads / kv_heads);  // per key head
+    if (M * q_heads <= idle || rows <= kKvFewRows) return 0x7fffffff;
+    if (rows > kKvFewRows * n_seqs) return kKvFewRows;
+    if ((M - n_seqs) * q_heads <= 2 * idle) return 0x7fffffff;
+    return idle / kv_heads > kKvFewRows ? int(idle / kv_heads) : kKvFewRows;
+}
+
 // Blocks of `rows` rows for the sequences of a call without a sum over them: sequence b owns
 // the items from kv_row_item(q0_b, b) to kv_row_item(q0_{b+1}, b + 1), at least
-// floor(n * group / rows) + 1 >= kv_tiles(n, group, rows) of them.
-WQ_HD int64_t kv_row_item(int q0, int b, int group, int rows) { return int64_t(q0) * group / rows + b; }
+// floor(n * group / rows) + 1 >= kv_tiles(n, group, rows) of them.  few > 0: that many for sequences
+// of more than `few` rows only, beside the multiples of `rows` one item for every few + 1 rows
+// instead of one a sequence.
+WQ_HD int64_t kv_row_item(int q0, int b, int group, int rows, int few = 0)
+{
+    const unsigned r = unsigned(q0) * unsigned(group);  // (below 2^31)
+    return int64_t(r / unsigned(rows)) + (few ? r / unsigned(few + 1) : unsigned(b));
+}
 
 // Block c of `grid` takes the units kv_share(c) .. kv_share(c + 1) - 1 of `total` (grid below 2^16).
 WQ_HD int kv_share(int total, int c, int grid)

@@ -947,7 +947,6 @@ RowsPlan rows_plan(int head_dim)
 }
 
 constexpr int kMostPerSm = 2;
-constexpr int kFewRows = 16;
 // two partial slots a block in the workspace's 64 KB per SM: two blocks of 8 rows of 132 binary32
 // values, or one of 8 rows of 260
 static_assert(2 * 2 * kRowsOfTile * (128 + 4) * 4 <= 65536 && 2 * kRowsOfTile * (256 + 4) * 4 <= 65536, "");
@@ -1048,18 +1047,20 @@ extern "C" wq_status kv_attention(const void *q, wq_dtype dt, int64_t M, int32_t
         a.partials = static_cast<float *>(workspace);
         a.arrivals = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) + ws_scratch_bytes());
     }
-    // Sequences with up to kFewRows rows per key head are bound by reading their keys once and go
-    // to the key-split kernel, the others to the tile kernel.  One launch where sequences bring that
-    // few rows on average, right for any distribution; and where the call's rows are so few that
-    // tiles would leave most SMs idle, even if each key is read for several tiles of 8 rows.
+    // Sequences with few rows per key head are bound by reading their keys once and go to the key-split
+    // kernel, the others to the tile kernel.  One launch where the call's rows are so few that tiles would
+    // leave most SMs idle, even if each key is read for several tiles of 8 rows, and for decode and draft
+    // batches (kv_few_rows).
     // Tiles against split, us: heads of 128, 3000 keys, 1280 rows in all 80 / 37, 3200 rows 83 / 69,
     // 6400 rows 79 / 119; 64 rows and 20000 keys 382 / 22; heads of 256, 1280 rows 88 / 51, 3200 rows
-    // 88 / 107.
+    // 88 / 107.  Both kernels against the split alone, single tokens over 1000 keys and a chunk among
+    // them, 32 query and key heads: 64 and 900 tokens 173 / 372, 200 and 2000 462 / 1110, 64 and 256 154 /
+    // 208; 256 and 512 of 8 key heads 172 / 262.  What the tile kernel costs a draft batch, of which it
+    // takes nothing: 64 sequences of 6 tokens 143.8 / 142.6, 512 of 2 960 / 950.
     const bool bf16 = dt == WQ_BF16, f8 = cache->format == WQ_FMT_E4M3;
     const int64_t idle = int64_t(a.head_dim <= 128 ? 24 : 16) * device_info().sm_count;
-    const bool tiles = M * a.group > kFewRows * batch->n_seqs && M * q_heads > idle;
-    a.few_rows = tiles ? kFewRows : 0x7fffffff;
-    if (tiles) {
+    a.few_rows = kv_few_rows(M, batch->n_seqs, q_heads, cache->kv_heads, idle);
+    if (a.few_rows != 0x7fffffff) {
         rc = kv_attn_tiles(a, bf16, f8, stream);
         if (rc != WQ_OK) return rc;
         a.behind_tiles = true;

@@ -19,6 +19,7 @@ struct KvAttnArgs {
     int page_shift, pitch, capacity;
     float sm_scale;
     int few_rows;         // sequences with more rows per key head go to the tile kernel
+    int by_rows;          // its items are counted by rows: few_rows, or 0 (see kv_row_item)
     // The kernel for few rows, launched behind the tile kernel of the same call, runs beside it: every
     // block of the tile kernel has waited for the kernels before when it lets the next grid start,
     // so the one started needs no wait of its own for them.  It waits for the tile kernel's end at
@@ -39,6 +40,6 @@ wq_status kv_attn_rows(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
 size_t kv_attn_rows_workspace();
 
 // Many rows per key head (prefill): 256-row tiles on the tensor cores (wq_kv_tiles.cu).
-wq_status kv_attn_tiles(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st);
+wq_status kv_attn_tiles(KvAttnArgs a, bool bf16, bool f8, cudaStream_t st);
 
 }  // namespace wq

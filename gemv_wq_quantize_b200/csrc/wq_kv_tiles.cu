@@ -729,7 +729,7 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     __shared__ Bars bar;
     __shared__ Scales sc;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, s_seq[4];
+    __shared__ int abort_flag, s_seq[6];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qsm = smem, *ksm = qsm + kRows / kTile * L::kQ, *vsm = ksm + 2 * L::kK;
     uint8_t *kraw = vsm + 2 * L::kV, *vraw = kraw + L::kRaw;
@@ -740,28 +740,33 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     const int64_t item = blockIdx.x / a.kv_heads;
     if (tid == 0) {
         s_seq[0] = -1;
+        s_seq[5] = 0;
         abort_flag = 0;
     }
     __syncthreads();
     for (int b = tid; b < a.n_seqs; b += kThreads) {
         const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
+        if (hi < lo) s_seq[5] = 1;  // offsets that decrease: no item's owner is certain, so nothing is done
         const KvSpan s = kv_span(lo, hi, len, a.M, a.capacity);
-        if (kv_row_item(s.q0, b, a.group, kRows) <= item && item < kv_row_item(s.q0 + s.n, b + 1, a.group, kRows)) {
+        const int64_t first = kv_row_item(s.q0, b, a.group, kRows, a.by_rows);
+        if (first <= item && item < kv_row_item(s.q0 + s.n, b + 1, a.group, kRows, a.by_rows)) {
             s_seq[0] = b;
             s_seq[1] = lo;
             s_seq[2] = hi;
             s_seq[3] = len;
+            s_seq[4] = int(item - first);
         }
     }
     __syncthreads();
     Item t;
     t.b = s_seq[0];
-    if (t.b < 0) return;
+    if (s_seq[5] && tid == 0) atomicCAS(&g_kv_tiles_error, kErrNone, kErrRange);
+    if (t.b < 0 || s_seq[5]) return;
     t.s = kv_span(s_seq[1], s_seq[2], s_seq[3], a.M, a.capacity);
     if (tid == 0 && s_seq[3] > a.capacity) atomicCAS(&g_kv_tiles_error, kErrNone, kErrRange);
     const int all = t.s.n * a.group;
     // the last rows first: they see the most keys
-    const int64_t k = kv_tiles(t.s.n, a.group, kRows) - 1 - (item - kv_row_item(t.s.q0, t.b, a.group, kRows));
+    const int64_t k = kv_tiles(t.s.n, a.group, kRows) - 1 - s_seq[4];
     if (k < 0 || all <= a.few_rows) return;
     t.head = blockIdx.x % a.kv_heads;
     t.row0 = int(k) * kRows;
@@ -843,13 +848,16 @@ TilesPlan tiles_plan(int head_dim)
 
 }  // namespace
 
-wq_status kv_attn_tiles(const KvAttnArgs &a, bool bf16, bool f8, cudaStream_t st)
+wq_status kv_attn_tiles(KvAttnArgs a, bool bf16, bool f8, cudaStream_t st)
 {
     const TilesPlan p = f8 ? (bf16 ? tiles_plan<true, true>(a.head_dim) : tiles_plan<true, false>(a.head_dim))
                            : (bf16 ? tiles_plan<false, true>(a.head_dim) : tiles_plan<false, false>(a.head_dim));
     if (cudaFuncSetAttribute(p.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem) != cudaSuccess)
         return check_launch("cudaFuncSetAttribute(kv_attn_tiles_kernel)");
-    const int64_t blocks = kv_row_item(a.M, a.n_seqs, a.group, p.rows) * a.kv_heads;
+    // whichever makes fewer blocks
+    const int64_t by_seq = kv_row_item(a.M, a.n_seqs, a.group, p.rows), by_rows = kv_row_item(a.M, 0, a.group, p.rows, a.few_rows);
+    a.by_rows = by_rows < by_seq ? a.few_rows : 0;
+    const int64_t blocks = std::min(by_seq, by_rows) * a.kv_heads;
     if (blocks > 0x7fffffff) return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
     CUtensorMap km, vm;
     wq_status rc = encode_cache(&km, &vm, a, std::min(1 << a.page_shift, p.keys));

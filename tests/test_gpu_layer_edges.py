@@ -185,3 +185,31 @@ def test_workspace_size_of_an_invalid_call_is_an_error():
     for M, heads in ((0, 4), (4, 3), (4, 0), (2 ** 30, 4)):
         with pytest.raises(wq.WqError):
             wq.kv_attention_workspace_size(M, heads, cache, batch)
+
+
+# ---------------------------------------------------------------- decode and a prompt chunk in one call
+MIXED = [
+    # new, total, q_heads, kv_heads, D
+    ([1] * 40 + [300], [50] * 40 + [420], 24, 24, 64),
+    ([1] * 20 + [300] + [1] * 20 + [0, 0, 30], [50] * 20 + [300] + [7] * 20 + [0, 9, 90], 24, 24, 128),
+    ([300] + [1] * 90 + [257], [290] + [33] * 90 + [500], 20, 10, 96),
+    ([1] * 30 + [0] * 5 + [260], [40] * 30 + [0] * 5 + [300], 24, 24, 256),
+    ([260, 1] + [2] * 40, [700, 90] + [33] * 40, 20, 20, 192),
+]
+
+
+@pytest.mark.parametrize("dtype,out", [("fp16", "int8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("case", MIXED, ids=lambda c: "s%d_h%d-%d_d%d" % (len(c[0]), c[2], c[3], c[4]))
+def test_attention_of_decode_and_a_chunk(case, dtype, out):
+    """A long run among single tokens (its rows on the tile kernel, the others beside them), and the same
+    bits as often as it runs."""
+    new, total, hq, hkv, D = case
+    idle = (24 if D <= 128 else 16) * torch.cuda.get_device_properties(0).multi_processor_count
+    assert (sum(new) - len(new)) * hq > 2 * idle and sum(new) * (hq // hkv) <= 16 * len(new)
+    s = Setup(new, total, hq, hkv, D, 32, dtype, out, seed=D, tail=3).fill(total)
+    cache, batch = s.device()
+    q = s.q()
+    got = _attend(s, q, cache, batch)
+    _attend_check(s, q, got)
+    for _ in range(3):
+        assert torch.equal(_attend(s, q, cache, batch), got)

@@ -3,6 +3,7 @@ arithmetic of the kernels (csrc/wq_kv.h, compiled here for the CPU) and the argu
 import ctypes
 import itertools
 import os
+import random
 import subprocess
 
 import pytest
@@ -21,6 +22,9 @@ void append_item(int lo, int hi, int len, int M, long long k, int sh, int limit,
     const KvPageSpan p = kv_page_span(kv_append_span(lo, hi, len, M), k, sh);
     o[0] = p.page; o[1] = p.off; o[2] = p.count ? kv_placed(p, sh, limit) : 0; o[3] = p.token; o[4] = p.count;
 }
+int few_rows(long long M, long long n, int q_heads, int kv_heads, long long idle) { return kv_few_rows(M, n, q_heads, kv_heads, idle); }
+long long row_item(int q0, int b, int group, int rows, int few) { return kv_row_item(q0, b, group, rows, few); }
+long long tiles(int n, int g, int r) { return kv_tiles(n, g, r); }
 }
 """
 
@@ -33,6 +37,9 @@ def kv(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "gemv_wq_quantize_b200", "csrc"), str(d / "kv.cpp"), "-o", str(so)], check=True)
     lib = ctypes.CDLL(str(so))
+    lib.few_rows.argtypes = [ctypes.c_longlong] * 2 + [ctypes.c_int] * 2 + [ctypes.c_longlong]
+    for f in (lib.row_item, lib.tiles):
+        f.restype = ctypes.c_longlong
     lib.append_item.argtypes = [ctypes.c_int] * 4 + [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
     return lib
 
@@ -52,6 +59,58 @@ def test_append_places_tokens_below_the_limit_only(kv, limit):
                 got[token + i] = page * 16 + off + i
         total = max(total, 0)
         assert got == {3 + i: total - n + i for i in range(n) if 0 <= total - n + i < limit}, (n, total)
+
+
+# ---------------------------------------------------------------- which attention kernel
+IDLE = 24 * 148
+
+
+@pytest.mark.parametrize("new,heads,tiled", [
+    # a prompt chunk among single tokens: the chunk's rows go to the tile kernel, the others do not
+    ([1] * 64 + [900], (32, 32), [900]),
+    ([1] * 64 + [900], (8, 8), [900]),
+    ([1] * 256 + [512], (32, 8), [512]),
+    ([1] * 200 + [2000], (32, 32), [2000]),
+    ([1] * 200 + [2000], (4, 4), [2000]),
+    ([1] * 64 + [256], (32, 32), [256]),
+    ([1] * 31 + [0] * 33 + [900], (32, 32), [900]),          # slots without tokens
+    # too few rows for it
+    ([1] * 64 + [100], (32, 32), []),
+    ([1] * 64 + [32], (32, 8), []),
+    ([40], (32, 32), []),
+    ([10], (1024, 1024), []),
+    # decode and draft batches
+    ([1] * 256, (32, 8), []),
+    ([1] * 248 + [0] * 8, (32, 32), []),
+    ([6] * 64, (32, 32), []),
+    ([2] * 512, (32, 32), []),
+    ([1] * 4096, (64, 1), [1] * 4096),                       # (64 rows each)
+    # prompts
+    ([300, 200, 1], (32, 8), [300, 200]),
+    ([20] * 16, (32, 32), [20] * 16),
+    ([2048, 2048], (32, 8), [2048, 2048]),
+])
+def test_long_sequences_go_to_the_tile_kernel(kv, new, heads, tiled):
+    few = kv.few_rows(sum(new), len(new), *heads, IDLE)
+    group = heads[0] // heads[1]
+    assert few >= 16 and [n for n in new if n * group > few] == tiled
+
+
+def test_row_blocks_counted_by_rows_cover_every_long_sequence(kv):
+    r = random.Random(0)
+    for _ in range(300):
+        group, rows, few = r.choice((1, 2, 5, 8)), r.choice((128, 256)), r.choice((16, 111, 444))
+        q0 = 0
+        for b in range(40):
+            n = r.choice((0, 1, 3, 17, 30, 112, 300, 2000))
+            first, end = kv.row_item(q0, b, group, rows, few), kv.row_item(q0 + n, b + 1, group, rows, few)
+            assert first <= end
+            if n * group > few:
+                assert end - first >= kv.tiles(n, group, rows)
+            q0 += n
+    # rows near 2^31
+    assert kv.row_item(2 ** 31 - 1, 4095, 1, 256, 16) == (2 ** 31 - 1) // 256 + (2 ** 31 - 1) // 17
+    assert kv.row_item(2 ** 28 - 1, 4095, 8, 128, 0) == (2 ** 31 - 8) // 128 + 4095
 
 
 # ---------------------------------------------------------------- refusals
