@@ -74,7 +74,9 @@ struct AppendArgs {
 // Four neighbouring values d .. d + 3 of a head row and their rotation.  Loads and arithmetic are
 // apart, and the loads of a row that does not turn (or of a lane behind the head) go to a valid
 // address and are not used: without branches around them the loads of many rows are in flight
-// before the first is worked on.
+// before the first is worked on.  Rows, batch arrays and scales are read with plain loads: the kernel
+// ahead may write them while this one is already resident, which the read-only path does not allow.
+// (The rope table is no such kernel's output.)
 struct Turn {
     float c[4], s[4];
 };
@@ -128,17 +130,17 @@ template <typename T, Mode MODE>
 __device__ __forceinline__ Raw load_raw(const AppendArgs &a, const T *row, int d)
 {
     Raw r;
-    r.x = __ldg(reinterpret_cast<const uint2 *>(row + d));
+    r.x = *reinterpret_cast<const uint2 *>(row + d);
     if constexpr (MODE == kHalf) {
         const int half = a.rope_dim / 2;
-        r.p = __ldg(reinterpret_cast<const uint2 *>(row + (d < half ? d + half : (d < a.rope_dim ? d - half : d))));
+        r.p = *reinterpret_cast<const uint2 *>(row + (d < half ? d + half : (d < a.rope_dim ? d - half : d)));
     } else if constexpr (MODE == kHalf2) {
         const int half = a.rope_dim / 2;
         uint32_t p[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int e = min(d + 2 * i, a.rope_dim - 2);
-            p[i] = __ldg(reinterpret_cast<const uint32_t *>(row + (e < half ? e + half : e - half)));
+            p[i] = *reinterpret_cast<const uint32_t *>(row + (e < half ? e + half : e - half));
         }
         r.p = make_uint2(p[0], p[1]);
     } else if constexpr (MODE == kAny) {
@@ -148,7 +150,7 @@ __device__ __forceinline__ Raw load_raw(const AppendArgs &a, const T *row, int d
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = min(d + i, a.rope_dim - 1);
-            p[i] = __ldg(w + (a.pairs ? (e ^ 1) : (e < half ? e + half : e - half)));
+            p[i] = w[a.pairs ? (e ^ 1) : (e < half ? e + half : e - half)];
         }
         r.p = make_uint2(p[0] | uint32_t(p[1]) << 16, p[2] | uint32_t(p[3]) << 16);
     }
@@ -322,7 +324,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int b, const Kv
     const int pos0 = (ps.page << a.page_shift) + ps.off;
     const int count = kv_placed(ps, a.page_shift, a.limit);
     const int64_t page =
-        count > 0 ? kv_page_ok(__ldg(a.block_table + int64_t(b) * a.max_pages + ps.page), a.c.num_pages) : -1;
+        count > 0 ? kv_page_ok(a.block_table[int64_t(b) * a.max_pages + ps.page], a.c.num_pages) : -1;
     if (tid == 0 && (page < 0 || count < ps.count)) atomicCAS(&g_kv_append_error, kErrNone, kErrRange);
     if (page < 0) return;
 
@@ -345,7 +347,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int b, const Kv
 template <typename T, bool F8, int CH, Mode MODE>
 __device__ __forceinline__ void append_few(const AppendArgs &a, int b, int part)
 {
-    const KvSpan span = kv_append_span(__ldg(a.cu_q + b), __ldg(a.cu_q + b + 1), __ldg(a.seq_len + b), a.M);
+    const KvSpan span = kv_append_span(a.cu_q[b], a.cu_q[b + 1], a.seq_len[b], a.M);
     if (span.n > kKvFewTokens) return;
 #pragma unroll 1
     for (int k = 0;; ++k) {

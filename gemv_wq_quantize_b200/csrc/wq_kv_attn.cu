@@ -244,7 +244,7 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs &a, const int *before, 
     }
     Tile t;
     t.b = lo;
-    t.s = kv_span(__ldg(a.cu_q + lo), __ldg(a.cu_q + lo + 1), __ldg(a.seq_len + lo), a.M, a.capacity);
+    t.s = kv_span(a.cu_q[lo], a.cu_q[lo + 1], a.seq_len[lo], a.M, a.capacity);
     const bool split = a.partials != nullptr;
     const int head_units = split ? kTileUnits : 0;
     const int units = split ? head_units + kv_units(t.s.len, shift) : 1;
@@ -335,7 +335,7 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const CUtensorMap
     Tile t;
     while (ok && share.next(t)) {
         const int32_t *table = a.block_table + int64_t(t.b) * a.max_pages;
-        auto entry_of = [&](int key) { return (boxed || grouped) && key < t.t1 ? __ldg(table + (key >> a.page_shift)) : 0; };
+        auto entry_of = [&](int key) { return (boxed || grouped) && key < t.t1 ? table[key >> a.page_shift] : 0; };
         const int n = steps_of(t);
         int entry = n ? entry_of(t.t0 + my_key) : 0;
         for (int j = 0; j < n; ++j) {
@@ -359,8 +359,8 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const CUtensorMap
                     tma_load_3d(sm.v[slot][c] + lane * box_rows * 128, vm, 128 * c, y, z, &sm.full[slot]);
                 }
             publish();
-            ks = grouped && z >= 0 ? __ldg(a.k_scale + z) : 0.f;
-            vs = grouped && z >= 0 ? __ldg(a.v_scale + z) : 0.f;
+            ks = grouped && z >= 0 ? a.k_scale[z] : 0.f;
+            vs = grouped && z >= 0 ? a.v_scale[z] : 0.f;
             bad = grouped && used && z < 0;
             pending = true;
             ++step;

@@ -189,7 +189,7 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, co
     const bool boxed = lane < boxes, grouped = lane >= kGroups && lane < 2 * kGroups;
     auto entry_of = [&](int step) {
         const int key = step * kKeys + my_key;
-        return (boxed || grouped) && key < t.keys ? __ldg(table + (key >> a.page_shift)) : 0;
+        return (boxed || grouped) && key < t.keys ? table[key >> a.page_shift] : 0;
     };
     int entry = entry_of(0), sent_k = 0, sent_v = 0;
     for (int j = 0; j < t.steps; ++j) {
@@ -199,8 +199,8 @@ __device__ __forceinline__ void copy_role(const KvAttnArgs &a, const Item &t, co
         const int z = page < 0 ? -1 : int(page) * a.kv_heads + t.head;
         float ks = 0.f, vs = 0.f;
         if (grouped && z >= 0) {
-            ks = __ldg(a.k_scale + z);
-            vs = __ldg(a.v_scale + z);
+            ks = a.k_scale[z];
+            vs = a.v_scale[z];
         }
         if (j + 1 < t.steps) entry = entry_of(j + 1);
         const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, boxed && z >= 0))) * uint32_t(box_rows * 128 * kBoxes);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int64_t j = tid + int64_t(i) * nt;
-            gv[i] = j < a.K8 ? __ldg(gamma + j) : make_uint4(0, 0, 0, 0);
+            gv[i] = j < a.K8 ? gamma[j] : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(const __gri
     } else {
         for (int64_t j = tid; j < a.K8; j += nt) {
             float y[8];
-            scaled8<T>(back[j], __ldg(gamma + j), rstd, y);
+            scaled8<T>(back[j], gamma[j], rstd, y);
             amax = absmax8(y, amax);
         }
     }
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kNormThreads) rmsnorm_quant_kernel(const __gri
     } else {
         for (int64_t j = tid; j < a.K8; j += nt) {
             float y[8];
-            scaled8<T>(back[j], __ldg(gamma + j), rstd, y);
+            scaled8<T>(back[j], gamma[j], rstd, y);
             q[j] = finite ? codes8<F8>(y, cs) : make_uint2(0, 0);
         }
     }

@@ -4,6 +4,7 @@ import ctypes
 import itertools
 import os
 import random
+import re
 import subprocess
 
 import pytest
@@ -155,3 +156,12 @@ def test_tensor_memory_is_taken_between_the_wait_and_the_next_launch(source):
         text = "\n".join(line.split("//")[0] for line in f)
     wait, take, launch = (text.index(w) for w in ("grid_dep_wait();", "tmem_alloc(", "grid_dep_launch();"))
     assert wait < take < launch
+
+
+@pytest.mark.parametrize("source", ["wq_norm.cu", "wq_kv_append.cu", "wq_kv_attn.cu", "wq_kv_tiles.cu"])
+def test_what_a_kernel_ahead_may_write_is_not_read_as_constant(source):
+    """These kernels are resident before the ones ahead have ended; the read-only path (__ldg) is for memory
+    that nobody writes meanwhile.  Only the rope table (`tab`) is."""
+    with open(os.path.join(ROOT, "gemv_wq_quantize_b200", "csrc", source)) as f:
+        text = f.read()
+    assert all(re.match(r"(reinterpret_cast<const float\d \*>\()?tab \+", rest) for rest in text.split("__ldg(")[1:])
