@@ -577,8 +577,11 @@ extern "C" wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t 
     const int64_t items = M > kKvFewTokens ? kv_item_start(int(M), int(batch->n_seqs), a.page_shift, runs) : 0;
     const int64_t all = items * 2 * cache->kv_heads, run_blocks = runs ? all : std::min<int64_t>(all, device_info().sm_count);
     // Queries, a block a token or a warp a token: 1024 tokens of 32 heads 13.2 / 14.5 us, 1600 19.2 /
-    // 19.5, 4096 48.5 / 39.3.
-    a.q_tokens = M <= 1600 ? 1 : kWarps;
+    // 19.5, 4096 48.5 / 39.3.  No more warps a token than heads: 256 tokens of one head 4.5 us with a
+    // block each, 3.3 with a warp each, of four heads 4.8 and with two warps 3.8.
+    int warps = 1;
+    while (warps < kWarps && warps < q_heads) warps *= 2;
+    a.q_tokens = M <= 1600 ? kWarps / warps : kWarps;
     const int64_t blocks = run_blocks + batch->n_seqs * a.parts + (M + a.q_tokens - 1) / a.q_tokens;
     if (std::max(all, blocks) > 0x7fffffff - device_info().sm_count)
         return fail(WQ_ERR_INVALID_ARG, "too many blocks: fewer rows or heads a call");
