@@ -176,6 +176,98 @@ def test_attention_huge_scores(D, many, dtype, out):
     assert np.isfinite(got).all() and (np.abs(got - want) <= lim).all()
 
 
+# ---------------------------------------------------------------- attention: what few rows keep of a weight
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+def test_few_rows_keep_small_weights(out, D):
+    """One key with the value 0 outweighs 6000 others by 2^18 to 2^25, whose values are all positive: the
+    result is what the small weights add up to."""
+    n = 6000
+    s = Setup([1], [n], 2, 1, D, 64, "bf16", out, seed=5).fill([n])
+    at = np.arange(n)
+    pages, slots = s.table[0, at // 64], at % 64
+    r = np.random.default_rng(2)
+    kc = np.zeros((n, D))
+    kc[:, 0] = r.integers(-20, 20, n)
+    kc[0, 0] = 120
+    vc = np.abs(ref.values_of(s.host.v[pages, 0, slots, :D], out))
+    vc[0] = 0
+    s.host.k[pages, 0, slots, :D] = ref.codes_of(kc, 1, out)
+    s.host.v[pages, 0, slots, :D] = ref.codes_of(vc, 1, out)
+    s.host.ks[:] = np.where(np.isfinite(s.host.ks), 1.0, s.host.ks)
+    q = np.zeros((1, 2, D))
+    q[..., 0] = 0.125, 0.1171875
+    cache, batch = s.device()
+    got = _np(_attend(s, ref.to_t(q, s.dt), cache, batch, sm_scale=1.0))
+    want, mass, score, top, _ = ref.attention_64(q, s.host, s.cu, s.total, s.table, 1.0, s.num_pages)
+    # A weight times its value scale is kept to half of 2^-26 (INT8) or to 2^-16 of itself and half of
+    # 2^-27 (e4m3), in units of a power of two that is at most twice the largest value scale; then
+    # the scores' and the exponentials' errors, and a sum per 128 keys.
+    rel = 2 * 2.0 ** -24 * score + 2.0 ** -20 + (n / 128 + 64) * 2.0 ** -24 + (2.0 ** -16 if out == "fp8" else 0)
+    lim = U["bf16"] * np.abs(want) + rel * mass + (2.0 ** -26 if out == "int8" else 2.0 ** -27) * top
+    assert (np.abs(got - want) <= 1.01 * lim).all(), np.max(np.abs(got - want) / lim)
+
+
+# ---------------------------------------------------------------- shapes
+@pytest.mark.parametrize("out", ["int8", "fp8"])
+@pytest.mark.parametrize("new,total,hq,hkv,D", [
+    ([1, 3, 1], [300, 90, 17], 64, 1, 128),
+    ([1, 1, 2], [300, 90, 17], 40, 2, 256),
+    ([80, 1, 20], [300, 90, 20], 64, 1, 128),
+    ([70, 1, 13], [300, 90, 20], 48, 2, 192),
+])
+def test_attention_of_large_groups(new, total, hq, hkv, D, out):
+    """Up to 64 query heads a key head, in both kernels."""
+    s = Setup(new, total, hq, hkv, D, 128, "bf16", out, seed=hq).fill(total)
+    cache, batch = s.device()
+    q = s.q()
+    _attend_check(s, q, _attend(s, q, cache, batch))
+
+
+@pytest.mark.parametrize("new", [[1, 4, 1], [200, 1, 90]])
+def test_a_cache_beyond_4_gigabytes(new):
+    """The same call in a small cache and in the last pages of one whose keys alone pass 2^32 bytes."""
+    s = Setup(new, [300, 40, 290], 16, 8, 256, 256, "fp16", "int8", seed=6)
+    s.fill([t - n for n, t in zip(new, s.total)])
+    far = 2 ** 32 // (8 * 256 * 256) + 1
+    if torch.cuda.mem_get_info()[0] < 3 * far * 8 * 256 * 256:
+        pytest.skip("needs 13 GB")
+    qkv, results = s.qkv(), []
+    for offset in (0, far):
+        cache, batch = s.device()
+        if offset:
+            big = wq.make_kv_cache(offset + s.num_pages, 256, 8, 256)
+            for name in ("k", "v", "k_scale", "v_scale"):
+                getattr(big, name)[offset:].copy_(getattr(cache, name))
+            batch.block_table.add_(offset)
+            cache = big
+        q = _append(s, qkv, s.rope(256), "half", cache, batch)
+        o = _attend(s, _np(q), cache, batch)
+        results.append([q, o] + [getattr(cache, n)[offset:].clone() for n in ("k", "v", "k_scale", "v_scale")])
+    torch.cuda.synchronize()
+    for a, b in zip(*results):
+        assert torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+# ---------------------------------------------------------------- queries that are not finite
+@pytest.mark.parametrize("dtype,out", [("fp16", "int8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("D,many", [(64, False), (256, False), (128, True), (256, True)])
+def test_attention_rows_beside_one_that_is_not_finite(D, many, dtype, out):
+    """An infinity or NaN spoils the row that holds it, and no other."""
+    new = [130, 40] if many else [3, 1]
+    s = Setup(new, [300, 90], *(_many(new, 2, 1) if many else (4, 2)), D, 32, dtype, out, seed=12).fill([300, 90])
+    q = s.q()
+    bad = np.zeros(q.shape[:2], bool)
+    bad[1, 0] = bad[2, 1] = bad[-1, 0] = True
+    x = q.copy()
+    x[1, 0, 3], x[2, 1, D - 1], x[-1, 0, 0] = np.nan, np.inf, -np.inf
+    cache, batch = s.device()
+    got = _np(_attend(s, x, cache, batch))
+    want, mass, score, top, _ = ref.attention_64(q, s.host, s.cu, s.total, s.table, float(np.float32(D ** -0.5)), s.num_pages)
+    lim = _bound(want, mass, score, top, 300, dtype)
+    assert (np.abs(got - want) <= lim)[~bad].all() and np.isnan(got[1, 0]).all()
+
+
 # ---------------------------------------------------------------- the binding
 def test_workspace_size_of_an_invalid_call_is_an_error():
     cache = wq.make_kv_cache(4, 16, 2, 64)
