@@ -18,9 +18,12 @@
 // queries.
 //
 // Bound by instruction issue for long runs (rotation, codes), else by the launch and the chain of
-// table, row, maximum and codes.  Measured, 32 query heads: 8192 tokens in six runs, 8 key heads of
-// 128: 38 us, 3.2 TB/s (108 us with branches around the loads and a division a code); 48 sequences of
-// 1 to 6 tokens, 32 key heads of 100: 8.1 us; 16 of one token, 32 key heads of 128: 3.6 us.
+// table, row, maximum and codes.  Measured (device time, calls back to back in a graph), 32 query heads:
+// 8192 tokens in six runs, 8 key heads of 128: 37 us, 3.2 TB/s (108 us with branches around the loads and a
+// division a code); 48 sequences of 1 to 6 tokens, 32 key heads of 100: 8.0 us; 16 of one token, 32 key
+// heads of 128: 3.5 us.  These repeat a call, so no page's scale grows.  Where it does, a warp re-codes the
+// page's earlier rows one after the other: 16 single tokens, filling pages of 16 from their start with
+// ever larger values, take 6.7 us a step, pages of 64 16.6.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -12,8 +12,10 @@
 //   q = 2^e (q1 + q2 / 16 + q3 / 256 + q4 / 4096)      e4m3 cache: each part the e4m3 value nearest
 //                                                       to what is left
 //   q = 2^e (q1 2^21 + q2 2^14 + q3 2^7 + q4)           INT8 cache: digits of a 28-bit integer
-// (exact for binary16 and bfloat16 down to 2^-27 of the row's largest value), and the weights in
-// [0, 1) likewise, to 2^-29.  The parts of all rows are the N side of both products,
+// (exact for binary16 and bfloat16 down to 2^-27 of the row's largest value), and the weights times
+// their value scales likewise: over a power of two that is at most twice the largest scale so far, to
+// 2^-27 (INT8), or to 2^-16 of each and 2^-28 (e4m3).  The parts of all rows are the N side of both
+// products,
 //   S^T[key][part, row] = K Q^T      A = 128 keys of codes (rows of dimensions),
 //   O^T[dimension][part, row] = V^T P^T      A = the values of 128 keys, read dimension-major,
 // with binary32 (e4m3) or exact int32 (INT8) accumulators in Tensor Memory, and the parts are put
@@ -30,11 +32,11 @@
 // partial sums in the workspace; the last block to arrive adds them in the order of their keys,
 // so the result does not depend on which block that is.
 //
-// Measured, 32 query heads: two sequences of 131000 keys, 8 key heads of 128: 93 us, 5.8 TB/s;
-// 32 of 100 to 4095 keys: 42 us, 3.2 TB/s; 16 of 2 to 6 tokens and 300 to 2000 keys, 32 key heads
-// of 100: 52 us, 2.0 TB/s; one of 512 keys, 32 key heads: 14 us, where a block's start (Tensor
-// Memory, shares, queries), one step and the joining of the parts follow one another.  Against
-// codes widened in registers (mma.sync, per-warp rings): 114, 43, 48 and 13 us.
+// Measured (device time, calls back to back in a graph), 32 query heads: two sequences of 131000 keys, 8
+// key heads of 128: 93 us, 5.8 TB/s (99 us each, 5.4 TB/s, by a caller's clock); 32 of 100 to 4095 keys:
+// 40 us, 3.4 TB/s, with heads of 256 64 us; 16 of 2 to 6 tokens and 300 to 2000 keys, 32 key heads of 100:
+// 49.5 us, 2.2 TB/s; one of 512 keys, 32 key heads: 14 us, where a block's start (Tensor Memory, shares,
+// queries), one to five steps and the joining of the parts follow one another.
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>

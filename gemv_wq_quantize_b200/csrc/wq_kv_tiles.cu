@@ -19,10 +19,11 @@
 //  * warp 13: brings the next block's codes into shared memory (TMA) and its scales.
 // Every wait is bounded; on expiry the block records an error, stops and frees its Tensor Memory.
 //
-// Measured: two chunks of 2048 tokens, 32 query and 8 key heads of 128, behind 4096 to 6000 keys:
-// 550 us, 755 TF/s.  Four of 1000 tokens behind 2000 keys, heads of 256: 588 us, 557 TF/s (3843 us by
-// the split kernel of wq_kv_attn.cu).  Five prompts of 100 to 1100 tokens, 32 heads: 85 us, where a
-// block's start and end are most of its 18 to 25 us.  Codes by TMA instead of by the widening warps'
+// Measured (device time, calls back to back in a graph): two chunks of 2048 tokens, 32 query and 8 key
+// heads of 128, behind 4096 to 6000 keys: 540 us, 768 TF/s.  Four of 1000 tokens behind 2000 keys, heads
+// of 256: 550 us, 596 TF/s (3843 us by the split kernel of wq_kv_attn.cu).  Five prompts of 100 to 1100
+// tokens, 32 heads: 70 us (84 us by a caller's clock), where a block's start and end are most of its 18
+// to 25 us.  While it was built: codes by TMA instead of by the widening warps'
 // own loads: 1050 -> 678 us for the chunks; weights in one pass where the references hold: 678 ->
 // 641; loops of the roles rolled, so that their code stays in the instruction cache: 93 -> 87 us for
 // the prompts.

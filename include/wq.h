@@ -273,7 +273,7 @@ wq_status rmsnorm_quant_fp8(const void *X, const void *residual, const void *gam
  *   k, v              [num_pages, kv_heads, page_size, pitch] bytes, pitch = head_dim rounded up
  *                     to a multiple of 16 (bytes head_dim .. pitch - 1 are neither written nor
  *                     used)
- *   k_scale, v_scale  [num_pages, kv_heads] binary32, finite and not negative
+ *   k_scale, v_scale  [num_pages, kv_heads] binary32, from 0 to 2^122 (kv_append writes no others)
  * page_size 16, 32, 64, 128 or 256; head_dim a multiple of 4 from 16 to 256; kv_heads 1 to 1024;
  * format WQ_FMT_INT (INT8) or WQ_FMT_E4M3.  k and v 16-byte aligned.  Nothing needs to be
  * cleared before first use. */
@@ -326,8 +326,8 @@ typedef struct {
  *   become the codes of value * (scale before / scale).  The codes of the new tokens are those
  *   of x / scale (as act_quant_int8 / act_quant_fp8), from the rotated binary32 values.
  *   Slots behind the new tokens are left as they were.  An infinite key or value is stored as
- *   the largest code, NaN as 0, and neither counts for the scale, so that one bad token does not
- *   reach its page's other tokens.
+ *   the largest code (0 where the scale is 0), NaN as 0, and neither counts for the scale, so that one
+ *   bad token does not reach its page's other tokens.
  * Bit-exact with any implementation of this text.  M * q_heads < 2^31. */
 #define WQ_ROPE_HALF 0
 #define WQ_ROPE_PAIRS 1
@@ -338,8 +338,12 @@ wq_status kv_append(const void *qkv, wq_dtype dt, int64_t M, int32_t q_heads, co
 /* Causal attention of the call's rows over the cached keys and values of their sequences (the
  * rows' own tokens included: append first):
  *   out[m, h] = sum_{j <= p} softmax_j(sm_scale * q[m,h] . k_j) v_j,  key head h / (q_heads / kv_heads)
- * with p the row's position; binary32 scores, softmax statistics and sums.
- *   q, out [M, q_heads * head_dim] of type dt (WQ_F16 or WQ_BF16); sm_scale finite.
+ * with p the row's position; binary32 scores, softmax statistics and sums.  Weights times their value
+ * scale are rounded before the second product, in units of the largest scale that the row sees: where a
+ * sequence brings many rows to binary16 (2^-11 of each), where it brings few to 2^-27 (INT8 cache) or
+ * 2^-16 of each (e4m3).
+ *   q, out [M, q_heads * head_dim] of type dt (WQ_F16 or WQ_BF16), q finite (an infinity or NaN spoils
+ *   the rows that hold it, no others); sm_scale finite.
  *   workspace: as for w4a16_gemm (kv_attention_workspace_size bytes, zero-filled once, shared by
  *   calls that do not overlap); lets few rows over long contexts spread over the whole GPU.
  *   NULL or too small: every key range is walked by one block.  (The size is 0 for arguments that the
