@@ -747,10 +747,12 @@ kv_attn_tiles_kernel(const __grid_constant__ CUtensorMap km, const __grid_consta
     __syncthreads();
     for (int b = tid; b < a.n_seqs; b += kThreads) {
         const int lo = a.cu_q[b], hi = a.cu_q[b + 1], len = a.seq_len[b];
-        if (hi < lo) s_seq[5] = 1;  // offsets that decrease: no item's owner is certain, so nothing is done
+        const bool some = lo < hi;  // (slots without tokens may have any offsets)
+        // a sequence that begins before the end of the last: no item's owner is certain, so nothing is done
+        if (some && a.cu_q[max(b - 1, 0)] > lo) s_seq[5] = 1;
         const KvSpan s = kv_span(lo, hi, len, a.M, a.capacity);
         const int64_t first = kv_row_item(s.q0, b, a.group, kRows, a.by_rows);
-        if (first <= item && item < kv_row_item(s.q0 + s.n, b + 1, a.group, kRows, a.by_rows)) {
+        if (some && first <= item && item < kv_row_item(s.q0 + s.n, b + 1, a.group, kRows, a.by_rows)) {
             s_seq[0] = b;
             s_seq[1] = lo;
             s_seq[2] = hi;

@@ -298,9 +298,9 @@ typedef struct {
  * What the host cannot check is checked on the device: a needed block-table entry outside
  * 0 .. num_pages - 1, or seq_len beyond max_pages * page_size or beyond the rope table, sets the
  * device error word to 3 (wq_device_error); the tokens concerned are left out, nothing is
- * accessed out of range, and results of those sequences are not valid.  cu_q does not decrease and
- * is cut to 0..M; sequences that overlap are not accessed out of range either, but their results
- * are not valid. */
+ * accessed out of range, and results of those sequences are not valid.  cu_q is cut to 0..M and does
+ * not decrease, but that slots behind the last sequence may have any offsets that give them no rows.
+ * Sequences that overlap are not accessed out of range either, but their results are not valid. */
 typedef struct {
     const int32_t *cu_q;
     const int32_t *seq_len;

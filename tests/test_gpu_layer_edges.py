@@ -176,6 +176,24 @@ def test_attention_huge_scores(D, many, dtype, out):
     assert np.isfinite(got).all() and (np.abs(got - want) <= lim).all()
 
 
+@pytest.mark.parametrize("new,hq,hkv,D", [([300, 1, 90], 16, 16, 64), ([1300, 1, 90], 4, 4, 64), ([130, 1], 32, 8, 256), ([3, 1], 4, 2, 64)])
+def test_offsets_behind_the_last_sequence_may_be_zero(new, hq, hkv, D):
+    """Slots without tokens behind the last sequence, their offsets left at 0 (or at anything without rows): the
+    same bits, in each kernel and the append."""
+    total = [n + 40 for n in new] + [9, 0]
+    s = Setup(new + [0, 0], total, hq, hkv, D, 32, "fp16", "int8", seed=D).fill([t - n for n, t in zip(new + [0, 0], total)])
+    qkv, got = s.qkv(), []
+    for tail in ([s.M, s.M], [0, 0], [5, 5], [s.M, 0]):
+        cache, batch = s.device()
+        batch.cu_q[-2:].copy_(torch.tensor(tail, dtype=torch.int32))
+        q = _append(s, qkv, None, "half", cache, batch)
+        got.append([q, _attend(s, _np(q), cache, batch), cache.k, cache.v, cache.k_scale, cache.v_scale])
+    torch.cuda.synchronize()
+    assert wq.device_error() == 0
+    for g in got[1:]:
+        assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(got[0], g))
+
+
 # ---------------------------------------------------------------- attention: what few rows keep of a weight
 @pytest.mark.parametrize("D", [64, 256])
 @pytest.mark.parametrize("out", ["int8", "fp8"])
